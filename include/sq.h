@@ -372,6 +372,72 @@ SQ_API sq_status sq_linear_noalloc(const void *x, sq_dtype in_dt, const float *s
                                    int64_t K, void *y, sq_dtype out_dt, sq_stream_t stream);
 
 /*
+ * Microscaled 4-bit linear layer (OCP microscaling formats, MXFP4), next to
+ * the int8 one: the same smoothing, half the weight bytes.
+ *
+ * Format.  A block of 32 consecutive values along K shares a scale 2^(b - 127)
+ * (b one byte, E8M0); each value is an E2M1 code, sign and one of 0, .5, 1, 1.5,
+ * 2, 3, 4, 6.  For the block's largest magnitude a (fp32, after smoothing):
+ *   b    = max(floor(log2 a) - 2 + 127, 0)      (0 for a zero block)
+ *   code = round_half_even(v / 2^(b - 127)) to E2M1, magnitudes above 6 to 6
+ * A block with a NaN or an infinity gets b = 255 (its values read back as NaN)
+ * and zero codes; products with it are NaN.  Unlike the int8 entry points,
+ * inputs therefore need not be finite.
+ *   codes  [rows, K / 2] bytes, row-major, value 2j in bits 0-3 of byte j.
+ *   scales in tiles of 128 rows x 4 blocks (512 bytes), the tiles of a row tile
+ *          contiguous along K: row r, block i at byte
+ *          ((r / 128) * ceil(K / 128) + i / 4) * 512 + (r % 32) * 16 +
+ *          (r % 128 / 32) * 4 + i % 4; padding rows and blocks hold 0 (the
+ *          quantisers write them).  sq_mx4_scale_size gives the bytes.
+ * K is a multiple of 32 and N of 16; rows, N and K are at most 2^24
+ * (SQ_ERR_UNSUPPORTED).  Pointers are 16-byte aligned as everywhere.
+ *
+ * sq_mx4_quant_act:    v = RN(x * RN(1 / s)) (one reciprocal a channel), or x
+ *                      when s is NULL.
+ * sq_mx4_quant_weight: v = RN(w * s), or w when s is NULL.
+ * sq_mx4_dequant:      the values codes and scales stand for, [rows, K] fp32 or
+ *                      bf16 (exact in both).
+ */
+SQ_API size_t sq_mx4_scale_size(int64_t rows, int64_t K);
+SQ_API sq_status sq_mx4_quant_act(const void *x, sq_dtype dt, int64_t M, int64_t K, const float *s, uint8_t *xq,
+                                  uint8_t *sx, sq_stream_t stream);
+SQ_API sq_status sq_mx4_quant_weight(const void *w, sq_dtype dt, int64_t N, int64_t K, const float *s, uint8_t *wq,
+                                     uint8_t *sw, sq_stream_t stream);
+SQ_API sq_status sq_mx4_dequant(const uint8_t *q, const uint8_t *sc, int64_t rows, int64_t K, void *out,
+                                sq_dtype out_dt, sq_stream_t stream);
+
+/*
+ * The product y[m, n] = sum_k x[m, k] w[n, k] of the values that the codes and
+ * scales stand for, on the block-scaled tensor cores (tcgen05 kind::mxf4),
+ * accumulated in fp32 and rounded once to out_dt.  The order of the sum is
+ * fixed by the sizes and the device, so equal calls give equal bits.
+ *   xq [M, K / 2], sx its scale tiles, wq [N, K / 2], sw its scale tiles,
+ *   y [M, N].
+ *   workspace: device scratch, any contents, 16-byte aligned, at least
+ *   sq_mx4_gemm_workspace_size(M, N, K) bytes (0 for M > 128: NULL is fine
+ *   then); calls that can run concurrently need separate workspaces, two
+ *   captured graphs included.
+ * Up to 128 tokens the weight is streamed by every SM and shared tiles are
+ * summed through the workspace; more tokens run on CTA pairs.
+ */
+SQ_API size_t sq_mx4_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+SQ_API sq_status sq_mx4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M,
+                             int64_t N, int64_t K, void *y, sq_dtype out_dt, void *workspace, size_t ws_bytes,
+                             sq_stream_t stream);
+
+/*
+ * The online linear layer in this format: sq_mx4_quant_act, then sq_mx4_gemm
+ * (two kernels, the second's launch overlapping the first).
+ *   x [M, K] dtype in_dt; s [K] fp32 or NULL; wq, sw from sq_mx4_quant_weight;
+ *   y [M, N] dtype out_dt; workspace as in sq_mx4_gemm, at least
+ *   sq_mx4_linear_workspace_size(M, N, K) bytes (it also holds x's codes).
+ */
+SQ_API size_t sq_mx4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+SQ_API sq_status sq_mx4_linear(const void *x, sq_dtype in_dt, const float *s, const uint8_t *wq, const uint8_t *sw,
+                               int64_t M, int64_t N, int64_t K, void *y, sq_dtype out_dt, void *workspace,
+                               size_t ws_bytes, sq_stream_t stream);
+
+/*
  * Device error word: synchronises `stream`, then reads and clears the error
  * word the kernels set when a bounded on-chip wait gives up, or when
  * sq_gptq_factor meets a non-positive pivot.  Returns SQ_OK, SQ_ERR_TIMEOUT

@@ -20,6 +20,11 @@ The raw entry points keep the C names and take caller-allocated outputs:
     sq_linear(x, s, wq, sw, y, workspace)
     sq_linear_workspace_size(M, N, K)
     sq_linear_noalloc(x, s, wq, sw, y)          no workspace, no allocation
+    sq_mx4_quant_act(x, s, xq, sx)              microscaled 4-bit (MXFP4): codes and scale tiles
+    sq_mx4_quant_weight(w, s, wq, sw)
+    sq_mx4_dequant(q, sc, out)
+    sq_mx4_gemm(xq, sx, wq, sw, y, workspace)
+    sq_mx4_linear(x, s, wq, sw, y, workspace)
     sq_device_status()
 
 ``calibrate``, ``prepare_weight`` and ``linear`` are conveniences that allocate
@@ -60,6 +65,14 @@ ABI_SYMBOLS = (
     "sq_linear",
     "sq_linear_workspace_size",
     "sq_linear_noalloc",
+    "sq_mx4_scale_size",
+    "sq_mx4_quant_act",
+    "sq_mx4_quant_weight",
+    "sq_mx4_dequant",
+    "sq_mx4_gemm_workspace_size",
+    "sq_mx4_gemm",
+    "sq_mx4_linear_workspace_size",
+    "sq_mx4_linear",
     "sq_device_status",
     "sq_selftest_wait_timeout",
 )
@@ -78,7 +91,7 @@ _lib = None
 
 def _declare(lib):
     P, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
-    E = ctypes.c_int
+    E, Z = ctypes.c_int, ctypes.c_size_t
     sig = {
         "sq_status_string": ([E], ctypes.c_char_p),
         "sq_version": ([], ctypes.c_int),
@@ -100,6 +113,14 @@ def _declare(lib):
         "sq_linear": ([P, E, P, P, P, I, I, I, P, E, P, ctypes.c_size_t, P], E),
         "sq_linear_workspace_size": ([I, I, I], ctypes.c_size_t),
         "sq_linear_noalloc": ([P, E, P, P, P, I, I, I, P, E, P], E),
+        "sq_mx4_scale_size": ([I, I], Z),
+        "sq_mx4_quant_act": ([P, E, I, I, P, P, P, P], E),
+        "sq_mx4_quant_weight": ([P, E, I, I, P, P, P, P], E),
+        "sq_mx4_dequant": ([P, P, I, I, P, E, P], E),
+        "sq_mx4_gemm_workspace_size": ([I, I, I], Z),
+        "sq_mx4_gemm": ([P, P, P, P, I, I, I, P, E, P, Z, P], E),
+        "sq_mx4_linear_workspace_size": ([I, I, I], Z),
+        "sq_mx4_linear": ([P, E, P, P, P, I, I, I, P, E, P, Z, P], E),
         "sq_device_status": ([P, ctypes.POINTER(ctypes.c_uint32)], E),
         "sq_selftest_wait_timeout": ([ctypes.c_uint32, P], E),
     }
@@ -321,6 +342,127 @@ def sq_linear_noalloc(x, s, wq, sw, y, stream=None):
                                    _ptr(y), _dtype_code(y), _stream(stream)))
 
 
+# ---------------------------------------------------------------------------
+# microscaled 4-bit (MXFP4): s may be None; codes are uint8 [rows, K / 2], scales
+# uint8 of sq_mx4_scale_size(rows, K) bytes in the tiles include/sq.h describes
+# ---------------------------------------------------------------------------
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _mx4_ptrs(rows: int, K: int, q, sc):
+    """Device pointers of codes and scales, their sizes checked against [rows, K]."""
+    torch = _torch()
+    _need(q.dtype is torch.uint8 and tuple(q.shape) == (rows, K // 2), f"codes: uint8 of shape {(rows, K // 2)}")
+    _need(sc.dtype is torch.uint8 and sc.numel() >= -(-rows // 128) * -(-K // 128) * 512,
+          f"scales: uint8 of sq_mx4_scale_size({rows}, {K}) bytes")
+    return _ptr(q), _ptr(sc)
+
+
+def _mx4_factors(s, K: int):
+    if s is None:
+        return None
+    _need(s.dtype is _torch().float32 and s.numel() == K, f"s: float32 of {K} values")
+    return _ptr(s)
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
+class _on_device_of:
+    """Makes the device of `t` the current one for a call (its current stream is the default)."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, t):
+        torch = _torch()
+        self.guard = None
+        if t.is_cuda and t.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _same_device(first, *others):
+    d = first.device
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors on {d} and {t.device}")
+
+
+def sq_mx4_scale_size(rows: int, K: int) -> int:
+    """Bytes of the scale tiles of a [rows, K] matrix."""
+    return int(lib().sq_mx4_scale_size(rows, K))
+
+
+def sq_mx4_quant_act(x, s, xq, sx, stream=None):
+    M, K = x.shape
+    _same_device(x, s, xq, sx)
+    with _on_device_of(x):
+        _check("sq_mx4_quant_act", lib().sq_mx4_quant_act(_ptr(x), _dtype_code(x), M, K, _mx4_factors(s, K),
+                                                          *_mx4_ptrs(M, K, xq, sx), _stream(stream)))
+
+
+def sq_mx4_quant_weight(w, s, wq, sw, stream=None):
+    N, K = w.shape
+    _same_device(w, s, wq, sw)
+    with _on_device_of(w):
+        _check("sq_mx4_quant_weight", lib().sq_mx4_quant_weight(_ptr(w), _dtype_code(w), N, K, _mx4_factors(s, K),
+                                                                *_mx4_ptrs(N, K, wq, sw), _stream(stream)))
+
+
+def sq_mx4_dequant(q, sc, out, stream=None):
+    """out [rows, K] (float32 or bfloat16): the values the codes stand for."""
+    rows, K = out.shape
+    _same_device(out, q, sc)
+    with _on_device_of(out):
+        _check("sq_mx4_dequant", lib().sq_mx4_dequant(*_mx4_ptrs(rows, K, q, sc), rows, K, _ptr(out), _dtype_code(out),
+                                                      _stream(stream)))
+
+
+def sq_mx4_gemm_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().sq_mx4_gemm_workspace_size(M, N, K))
+
+
+def sq_mx4_gemm(xq, sx, wq, sw, y, workspace=None, stream=None):
+    """y [M, N] = x w^T of the values the codes stand for (a workspace is allocated when none is given)."""
+    M, N = y.shape
+    K = xq.shape[1] * 2
+    _same_device(y, xq, sx, wq, sw, workspace)
+    with _on_device_of(y):
+        if workspace is None:
+            workspace = _torch().empty(sq_mx4_gemm_workspace_size(M, N, K), dtype=_torch().uint8, device=y.device)
+        _check("sq_mx4_gemm", lib().sq_mx4_gemm(*_mx4_ptrs(M, K, xq, sx), *_mx4_ptrs(N, K, wq, sw), M, N, K, _ptr(y),
+                                                _dtype_code(y), *_ws_args(workspace), _stream(stream)))
+
+
+def sq_mx4_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().sq_mx4_linear_workspace_size(M, N, K))
+
+
+def sq_mx4_linear(x, s, wq, sw, y, workspace=None, stream=None):
+    """y [M, N] = mx4(x / s) w^T (a workspace is allocated when none is given)."""
+    M, K = x.shape
+    N = wq.shape[0]
+    _same_device(x, s, wq, sw, y, workspace)
+    _need(tuple(y.shape) == (M, N), f"y: shape {(M, N)}")
+    with _on_device_of(x):
+        if workspace is None:
+            workspace = _torch().empty(sq_mx4_linear_workspace_size(M, N, K), dtype=_torch().uint8, device=x.device)
+        _check("sq_mx4_linear", lib().sq_mx4_linear(_ptr(x), _dtype_code(x), _mx4_factors(s, K),
+                                                    *_mx4_ptrs(N, K, wq, sw), M, N, K, _ptr(y), _dtype_code(y),
+                                                    *_ws_args(workspace), _stream(stream)))
+
+
 def sq_device_status(stream=None) -> Tuple[int, int]:
     code = ctypes.c_uint32(0)
     st = lib().sq_device_status(_stream(stream), ctypes.byref(code))
@@ -368,4 +510,33 @@ def linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     sq_linear(x, s, wq, sw, y, workspace if need else None, stream)
+    return y
+
+
+def mx4_quantize(x, s=None, stream=None):
+    """Codes and scale tiles of the activations x [M, K], divided by s when given: returns (xq, sx)."""
+    torch = _torch()
+    M, K = x.shape
+    xq = torch.empty(M, K // 2, dtype=torch.uint8, device=x.device)
+    sx = torch.empty(sq_mx4_scale_size(M, K), dtype=torch.uint8, device=x.device)
+    sq_mx4_quant_act(x, s, xq, sx, stream)
+    return xq, sx
+
+
+def mx4_prepare_weight(w, s=None, stream=None):
+    """Codes and scale tiles of a weight [N, K] (times s when given), or of each of the experts' weights [E, N, K]:
+    returns (wq, sw), [N, K / 2] and [bytes] or [E, N, K / 2] and [E, bytes]."""
+    torch = _torch()
+    N, K = w.shape[-2:]
+    wq = torch.empty(*w.shape[:-1], K // 2, dtype=torch.uint8, device=w.device)
+    sw = torch.empty(*w.shape[:-2], sq_mx4_scale_size(N, K), dtype=torch.uint8, device=w.device)
+    for one, q, sc in zip(*(t.reshape(-1, *t.shape[-d:]) for t, d in ((w, 2), (wq, 2), (sw, 1)))):
+        sq_mx4_quant_weight(one, s, q, sc, stream)
+    return wq, sw
+
+
+def mx4_linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
+    """y = mx4(x / s) w^T with a torch-allocated output."""
+    y = _torch().empty(x.shape[0], wq.shape[0], dtype=out_dtype or x.dtype, device=x.device)
+    sq_mx4_linear(x, s, wq, sw, y, workspace, stream)
     return y

@@ -1,14 +1,16 @@
 """Build step for libsq.so, the CUDA library behind the C ABI in include/sq.h.
 
-Compiles the single translation unit csrc/sq_api.cu for sm_100a with nvcc into
-``libsq.so`` next to this file (in-tree, so it travels with the source tree).
-cudart is linked statically; only the ABI symbols are exported.
+Compiles the translation units of csrc/ (sq_api.cu: the int8 layer, sq_mx4_api.cu:
+the microscaled 4-bit operators) for sm_100a with nvcc, side by side, and links
+them into ``libsq.so`` next to this file (in-tree, so it travels with the source
+tree).  cudart is linked statically; only the ABI symbols are exported.
 
     python -m w8a8_int8_gemm_channel_b200._build [--force] [-v]
 """
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -19,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsq.so")
 MAIN = os.path.join(CSRC, "sq_api.cu")
+UNITS = [MAIN, os.path.join(CSRC, "sq_mx4_api.cu")]
+OBJ = os.path.join(PKG, "_build.d")  # object files, kept between builds (their names hold the process id until done)
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = [
@@ -29,10 +33,8 @@ NVCC_FLAGS = [
     "--expt-relaxed-constexpr",
     "-Xcompiler",
     "-fPIC,-fvisibility=hidden",
-    "-shared",
-    "-cudart",
-    "static",
 ]
+LINK_FLAGS = ["-shared", "-cudart", "static", "-ldl", "-lrt", "-lpthread"]
 
 
 def nvcc() -> str:
@@ -53,13 +55,55 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _headers(unit, seen=None):
+    """The headers of csrc/ and include/ that a unit includes, directly or through one another."""
+    seen = set() if seen is None else seen
+    with open(unit) as f:
+        names = re.findall(r'^#include "([^"]+)"', f.read(), re.M)
+    for name in names:
+        for d in (CSRC, INCLUDE):
+            p = os.path.join(d, name)
+            if os.path.exists(p) and p not in seen:
+                seen.add(p)
+                _headers(p, seen)
+    return seen
+
+
+def _object(unit):
+    return os.path.join(OBJ, os.path.basename(unit)[:-3] + ".o")
+
+
+def _object_stale(unit) -> bool:
+    obj = _object(unit)
+    if not os.path.exists(obj):
+        return True
+    t = os.path.getmtime(obj)
+    return any(os.path.getmtime(s) > t for s in [unit, *_headers(unit)])
+
+
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     """Compile libsq.so if it is missing or older than any source; return its path."""
     if not force and not stale():
         return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    running = []
+    for unit in UNITS:
+        if force or extra or _object_stale(unit):
+            tmp = _object(unit) + f".tmp{os.getpid()}.o"
+            cmd = [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, "-c", "-o", tmp, unit]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append((subprocess.Popen(cmd), cmd, tmp, _object(unit)))
+    failed = None
+    for p, cmd, tmp, obj in running:
+        if p.wait() != 0:
+            failed = failed or subprocess.CalledProcessError(p.returncode, cmd)
+        else:
+            os.replace(tmp, obj)
+    if failed:
+        raise failed
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, "-o", tmp, MAIN, "-ldl", "-lrt",
-           "-lpthread"]
+    cmd = [nvcc(), *ARCH, "-o", tmp, *map(_object, UNITS), *LINK_FLAGS]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)

@@ -1,0 +1,271 @@
+// sq_mx4.cuh -- the microscaled 4-bit format (OCP MXFP4): quantiser and
+// read-back.
+//
+// A block of 32 consecutive values along K shares one scale 2^(b - 127) (b a
+// byte, E8M0) and each value is an E2M1 code: sign, then 0, .5, 1, 1.5, 2, 3,
+// 4, 6.  For a block with largest magnitude a
+//   b    = max(e - 2, 0), e the biased fp32 exponent of a, so a / scale is in [4, 8)
+//   code = the nearest E2M1 value of v / scale, ties to the even code, at most 6
+// and a block that holds a NaN or an infinity gets b = 255 (NaN) and zero codes.
+// 1 / scale is a normal power of two, so v / scale is exact (or underflows to a
+// value that rounds to 0 anyway): the only rounding is the code's.
+//
+// Layout.  Codes [rows, K / 2] bytes, the even one of a pair in the low half.
+// Scale bytes in tiles of 128 rows x 4 blocks, 512 bytes a tile, the tiles of
+// one row tile contiguous along K: byte (r % 32) * 16 + (r % 128 / 32) * 4 +
+// block % 4 of tile (r / 128, block / 4).  Padding rows and blocks hold 0.
+// That is the order in which one tcgen05.cp moves a tile into tensor memory for
+// the block-scaled MMA, so no kernel reorders a scale.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sq_ptx.cuh"
+
+namespace sq {
+
+constexpr int kMx4Block = 32;        // values that share a scale
+constexpr int kMx4TileBytes = 512;   // scale bytes of 128 rows x 4 blocks
+constexpr int kMx4Threads = 256;
+
+enum : int { MX4_PLAIN = 0, MX4_TIMES = 1, MX4_OVER = 2 };  // v, v * s, v * RN(1 / s)
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// 8 consecutive values of dtype T as fp32
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void bf16x8_to_f32(const uint4 &u, float (&v)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8])
+{
+    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p)), v);
+}
+
+// Eight values scaled by `inv` as E2M1 codes, value i in bits 4i..4i+3.
+__device__ __forceinline__ uint32_t mx4_codes8(const float (&v)[8], float inv)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(d)
+        : "f"(v[0] * inv), "f"(v[1] * inv), "f"(v[2] * inv), "f"(v[3] * inv), "f"(v[4] * inv), "f"(v[5] * inv),
+          "f"(v[6] * inv), "f"(v[7] * inv));
+    return d;
+}
+
+// Scale byte of a block whose largest magnitude is `top` (NaN or infinity: 255).
+__device__ __forceinline__ uint32_t mx4_scale_byte(float top)
+{
+    const uint32_t e = __float_as_uint(top) >> 23;
+    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// 1 / scale of a finite block's byte: a normal power of two (byte <= 252)
+__device__ __forceinline__ float mx4_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// The scale a byte stands for (byte 0 is subnormal in fp32, 255 a NaN).
+__device__ __forceinline__ float mx4_scale(uint32_t byte)
+{
+    return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : (byte == 0u ? 0x00400000u : byte << 23));
+}
+
+// Offset of the word that holds the four scale bytes of row r in tile (r / 128, kt).
+__host__ __device__ __forceinline__ int64_t mx4_scale_word(int64_t r, int64_t kt, int64_t KT)
+{
+    return ((r >> 7) * KT + kt) * kMx4TileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+// One row's 8 values in each of 16 neighbouring lanes (128 values, 4 blocks;
+// all 32 lanes take part): writes the codes and, from the first of the 16, the
+// word of scale bytes.  A block is the 8 values of each of 4 lanes.
+__device__ __forceinline__ void mx4_store_chunk(const float (&v)[8], bool in_k, uint32_t *codes, uint32_t *word)
+{
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max_nan(top, fabsf(v[i]));
+    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    uint32_t byte = mx4_scale_byte(top);
+    const uint32_t c = byte == 255u ? 0u : mx4_codes8(v, mx4_inv_scale(byte));
+    if (in_k)
+        *codes = c;
+    else
+        byte = 0u;
+    byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+    byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 8) << 16;
+    if (word != nullptr)
+        *word = byte;
+}
+
+// Zero scale bytes of the padding rows behind row `rows`: word i of them for
+// this thread and every `step`-th after it.
+__device__ __forceinline__ void mx4_zero_pad(uint8_t *scales, int64_t rows, int64_t KT, int64_t i, int64_t step)
+{
+    const int64_t n = (((rows + 127) & ~int64_t{127}) - rows) * KT;
+    for (; i < n; i += step)
+        *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(rows + i / KT, i % KT, KT)) = 0u;
+}
+
+// Quantiser.  A thread owns 8 columns (its factors stay in registers) and
+// walks down the rows of its band, U rows in flight; 16 neighbouring threads
+// make one word of scale bytes.  A CTA covers TX * 8 columns, TX a multiple of
+// 16, and 256 / TX rows at a time.  Memory-bound: 2 or 4 bytes in and 17/32 out
+// a value; the smoothing divides by multiplying with RN(1 / s), one division a
+// column and band instead of one a value.
+// `zero`: counters of the GEMM after it, cleared on the side.
+template <typename T, int OP>
+__global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restrict__ x, int64_t rows, int64_t K,
+                                                                const float *__restrict__ s,
+                                                                uint8_t *__restrict__ codes,
+                                                                uint8_t *__restrict__ scales, int log2tx,
+                                                                int64_t band, int *__restrict__ zero, int nzero)
+{
+    pdl_prologue();
+    constexpr int U = 4;
+    const int tx = threadIdx.x & ((1 << log2tx) - 1), ty = threadIdx.x >> log2tx;
+    const int TY = kMx4Threads >> log2tx;
+    const int64_t KT = (K + 127) >> 7;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) << log2tx) + tx;  // chunk of 8 columns
+    const int64_t kt = c >> 4;
+    const bool in_k = c * 8 < K;
+    const bool word_lane = (threadIdx.x & 15) == 0 && kt < KT;
+    float f[8];
+    if constexpr (OP != MX4_PLAIN) {
+        if (in_k)
+            load8<float>(s + c * 8, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = !in_k ? 1.0f : (OP == MX4_OVER ? __frcp_rn(f[i]) : f[i]);
+    }
+    const int64_t r0 = blockIdx.y * band, r1 = min(rows, r0 + band);
+    // every lane of a warp takes the same trips (rows behind the end are
+    // clamped for the loads and not stored), so the shuffles are whole
+    for (int64_t rb = r0; rb < r1; rb += static_cast<int64_t>(TY) * U) {
+        float v[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = rb + ty + static_cast<int64_t>(u) * TY;
+            if (in_k && r < r1) {
+                load8<T>(x + r * K + c * 8, v[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[u][i] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = rb + ty + static_cast<int64_t>(u) * TY;
+            if constexpr (OP != MX4_PLAIN) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[u][i] = __fmul_rn(v[u][i], f[i]);
+            }
+            const bool live = r < r1;
+            mx4_store_chunk(v[u], in_k && live, reinterpret_cast<uint32_t *>(codes + r * (K / 2) + c * 4),
+                            word_lane && live ? reinterpret_cast<uint32_t *>(scales + mx4_scale_word(r, kt, KT))
+                                              : nullptr);
+        }
+    }
+    const int64_t nt = static_cast<int64_t>(gridDim.x) * gridDim.y * kMx4Threads;
+    const int64_t me = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kMx4Threads + threadIdx.x;
+    mx4_zero_pad(scales, rows, KT, me, nt);
+    for (int64_t i = me; i < nzero; i += nt)
+        zero[i] = 0;
+}
+
+// E2M1 pairs of one byte as two halves (exact)
+__device__ __forceinline__ __half2 e2m1x2_to_half2(uint32_t byte)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b8 b;\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tmov.b16 {b, _}, t;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+        : "=r"(d)
+        : "r"(byte));
+    return *reinterpret_cast<__half2 *>(&d);
+}
+
+// The values the codes stand for: 8 codes (4 bytes) a thread, U rows in flight,
+// the same walk as the quantiser.  E2M1 times a power of two is exact in fp32
+// and in bf16 (subnormal ones included).
+template <typename T>
+__global__ void __launch_bounds__(kMx4Threads) mx4_dequant_kernel(const uint8_t *__restrict__ codes,
+                                                                  const uint8_t *__restrict__ scales, int64_t rows,
+                                                                  int64_t K, T *__restrict__ out, int log2tx,
+                                                                  int64_t band)
+{
+    pdl_prologue();
+    constexpr int U = 4;
+    const int tx = threadIdx.x & ((1 << log2tx) - 1), ty = threadIdx.x >> log2tx;
+    const int TY = kMx4Threads >> log2tx;
+    const int64_t KT = (K + 127) >> 7;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) << log2tx) + tx;
+    if (c * 8 >= K)
+        return;
+    const int64_t r0 = blockIdx.y * band, r1 = min(rows, r0 + band);
+    for (int64_t rb = r0 + ty; rb < r1; rb += static_cast<int64_t>(TY) * U) {
+        uint32_t q[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = min(rb + static_cast<int64_t>(u) * TY, r1 - 1);
+            q[u] = __ldg(reinterpret_cast<const uint32_t *>(codes + r * (K / 2) + c * 4));
+            b[u] = __ldg(scales + mx4_scale_word(r, c >> 4, KT) + ((c >> 2) & 3));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = rb + static_cast<int64_t>(u) * TY;
+            if (r >= r1)
+                break;
+            const float sc = mx4_scale(b[u]);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 p = __half22float2(e2m1x2_to_half2((q[u] >> (8 * i)) & 0xFFu));
+                v[2 * i] = __fmul_rn(p.x, sc);
+                v[2 * i + 1] = __fmul_rn(p.y, sc);
+            }
+            T *dst = out + r * K + c * 8;
+            if constexpr (sizeof(T) == 4) {
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
+}  // namespace sq

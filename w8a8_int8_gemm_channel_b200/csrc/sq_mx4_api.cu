@@ -1,0 +1,367 @@
+// sq_mx4_api.cu -- the microscaled 4-bit entry points of the C ABI (declared
+// in include/sq.h): argument validation on the host, tensor maps and launches.
+// No entry point allocates memory; no C++ exception crosses the interface.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+
+#include "sq.h"
+#include "sq_host.cuh"
+#include "sq_mx4.cuh"
+#include "sq_mx4_gemm.cuh"
+#include "sq_mx4_stream.cuh"
+
+namespace sq {
+
+cudaError_t mx4_take_device_error(unsigned int *code)
+{
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_sq_device_error, sizeof *code);
+    if (e == cudaSuccess)
+        e = cudaMemcpyToSymbol(g_sq_device_error, &zero, sizeof zero);
+    return e;
+}
+
+}  // namespace sq
+
+namespace {
+
+using sq::OUT_BF16;
+using sq::OUT_F32;
+
+inline size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+inline bool ok_ptr(const void *p) { return p != nullptr && aligned16(p); }
+
+constexpr int64_t kMx4MaxDim = int64_t{1} << 24;  // rows and columns: TMA coordinates and the kernels' int sizes
+
+inline bool mx4_dims(int64_t rows, int64_t K) { return rows >= 1 && K >= 32 && K % 32 == 0; }
+
+inline size_t scale_bytes(int64_t rows, int64_t K)
+{
+    return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((K + 127) / 128) * sq::kMx4TileBytes;
+}
+
+// ---- quantiser and read-back ---------------------------------------------------
+// The CTA covers 2^log2tx chunks of 8 columns; the row bands fill every SM
+// about eight times over.
+struct Mx4Walk {
+    int log2tx;
+    unsigned gx, gy;
+    int64_t band;
+};
+
+inline Mx4Walk mx4_walk(int64_t rows, int64_t K, int64_t sms)
+{
+    Mx4Walk w;
+    const int64_t chunks = (K + 127) / 128 * 16;
+    w.log2tx = chunks <= 16 ? 4 : 5;
+    const int64_t TX = int64_t{1} << w.log2tx, step = sq::kMx4Threads / TX * 4;
+    const int64_t gx = (chunks + TX - 1) / TX;
+    const int64_t want = std::max<int64_t>(1, sms * 8 / gx);
+    w.band = std::max<int64_t>(step, ((rows + want - 1) / want + step - 1) / step * step);
+    while ((rows + w.band - 1) / w.band > 65535)
+        w.band *= 2;
+    w.gx = static_cast<unsigned>(gx);
+    w.gy = static_cast<unsigned>((rows + w.band - 1) / w.band);
+    return w;
+}
+
+template <typename T>
+sq_status launch_mx4_quant(const T *x, int64_t rows, int64_t K, const float *s, int op, uint8_t *q, uint8_t *sc,
+                           cudaStream_t st, int *zero = nullptr, int nzero = 0)
+{
+    DeviceInfo di;
+    if (!device_info(di))
+        return SQ_ERR_CUDA;
+    const Mx4Walk w = mx4_walk(rows, K, di.sms);
+    auto kernel = s == nullptr ? sq::mx4_quant_kernel<T, sq::MX4_PLAIN>
+                               : (op == sq::MX4_TIMES ? sq::mx4_quant_kernel<T, sq::MX4_TIMES>
+                                                      : sq::mx4_quant_kernel<T, sq::MX4_OVER>);
+    return launch_kernel(kernel, dim3(w.gx, w.gy), dim3(sq::kMx4Threads), 0, st, 0, 0, x, rows, K, s, q, sc, w.log2tx,
+                         w.band, zero, nzero);
+}
+
+sq_status mx4_quant(const void *x, sq_dtype dt, int64_t rows, int64_t K, const float *s, int op, uint8_t *q, uint8_t *sc,
+                    cudaStream_t st, int *zero = nullptr, int nzero = 0)
+{
+    return dt == SQ_BF16
+               ? launch_mx4_quant(static_cast<const __nv_bfloat16 *>(x), rows, K, s, op, q, sc, st, zero, nzero)
+               : launch_mx4_quant(static_cast<const float *>(x), rows, K, s, op, q, sc, st, zero, nzero);
+}
+
+sq_status check_mx4_quant(const void *x, sq_dtype dt, int64_t rows, int64_t K, const float *s, const void *q,
+                          const void *sc)
+{
+    if (!ok_ptr(x) || !valid_dtype(dt) || !mx4_dims(rows, K) || !aligned16(s) || !ok_ptr(q) || !ok_ptr(sc))
+        return SQ_ERR_INVALID_ARG;
+    if (rows > kMx4MaxDim || K > kMx4MaxDim)
+        return SQ_ERR_UNSUPPORTED;
+    return SQ_OK;
+}
+
+// ---- products ------------------------------------------------------------------
+// codes [rows, K / 2]: box of 128 bytes x box_rows rows, 128-byte swizzle
+bool make_tmap_mx4(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t K, int box_rows)
+{
+    return make_tmap_i8(map, codes, rows, K / 2, box_rows);
+}
+
+// scale tiles [row tiles, k tiles, 512 bytes]: box of box_rt row tiles x 2 k
+// tiles, a tile's 512 bytes contiguous; zeros outside
+bool make_tmap_scales(CUtensorMap *map, const uint8_t *scales, int64_t row_tiles, int64_t K, int box_rt)
+{
+    auto fn = encode_fn();
+    if (fn == nullptr)
+        return false;
+    const int64_t KT = (K + 127) / 128;
+    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(KT), static_cast<cuuint64_t>(row_tiles)};
+    cuuint64_t strides[2] = {512, static_cast<cuuint64_t>(KT * 512)};
+    cuuint32_t box[3] = {128, 2, static_cast<cuuint32_t>(box_rt)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(scales), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+constexpr int64_t kMx4MaxCtas = 160;  // of the streaming kernel: at least the SM count of every sm_100 part
+
+inline int mx4_bnx(int64_t M) { return M <= 32 ? 32 : (M <= 64 ? 64 : 128); }
+
+// Workspace of the product for few tokens: a counter for each tile of 128
+// channels, then two partial tiles a CTA.  More tokens need none.
+struct Mx4Ws {
+    size_t cnt = 0, slots = 0, total = 0;
+    int ncnt = 0;
+};
+
+inline Mx4Ws mx4_ws(int64_t M, int64_t N, size_t base)
+{
+    Mx4Ws w;
+    w.total = base;
+    if (M > sq::kMx4MaxTokens)
+        return w;
+    w.ncnt = static_cast<int>((N + 127) / 128);
+    w.cnt = base;
+    w.slots = base + round256(static_cast<size_t>(w.ncnt) * sizeof(int));
+    w.total = w.slots + static_cast<size_t>(kMx4MaxCtas) * 2 * mx4_bnx(M) * 128 * sizeof(float);
+    return w;
+}
+
+template <int BNX, int OUT>
+sq_status launch_mx4_stream(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M,
+                            int64_t N, int64_t K, void *y, int *cnt, float *slots, cudaStream_t st)
+{
+    using Cfg = sq::Mx4StreamCfg<BNX>;
+    DeviceInfo di;
+    if (!device_info(di))
+        return SQ_ERR_CUDA;
+    auto kernel = sq::mx4_stream_kernel<BNX, OUT, false>;
+    static std::atomic<uint64_t> attr_done{0};
+    if (!ensure_smem_attr(kernel, kMaxDynSmem, attr_done))
+        return SQ_ERR_CUDA;
+    CUtensorMap tw, tsw, tx, tsx;
+    if (!make_tmap_mx4(&tw, wq, N, K, 128) || !make_tmap_scales(&tsw, sw, (N + 127) / 128, K, 1) ||
+        !make_tmap_mx4(&tx, xq, M, K, BNX) || !make_tmap_scales(&tsx, sx, 1, K, 1))
+        return SQ_ERR_CUDA;
+    const int64_t T = (N + 127) / 128, KB = (K + sq::kMx4KB - 1) / sq::kMx4KB;
+    const int64_t G = stream_ctas(M, T, KB, std::min<int64_t>(di.sms, kMx4MaxCtas));
+    const int stages = Cfg::MAX_STAGES;
+    const int smem = sq::mx4_stream_smem(Cfg::STAGE_BYTES, stages, false);
+    static_assert(sq::mx4_stream_smem(Cfg::STAGE_BYTES, Cfg::MAX_STAGES, false) <= kMaxDynSmem, "shared memory");
+    if (debug_plan())
+        std::fprintf(stderr, "sq mx4 stream M=%lld N=%lld K=%lld: BNX=%d ctas=%lld stages=%d\n", (long long)M,
+                     (long long)N, (long long)K, BNX, (long long)G, stages);
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(G)), dim3(sq::kDecThreads), smem, st, 0, 0, tw, tsw, tx,
+                         tsx, y, slots, cnt, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
+                         static_cast<int>(G), stages, 0, sq::Mx4MoeArgs{});
+}
+
+template <int BN, int OUT>
+sq_status launch_mx4_pair_cfg(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M,
+                              int64_t N, int64_t K, void *y, cudaStream_t st)
+{
+    using Cfg = sq::Mx4PairCfg<BN>;
+    auto kernel = sq::mx4_pair_kernel<BN, OUT>;
+    static std::atomic<uint64_t> attr_done{0};
+    if (!ensure_smem_attr(kernel, Cfg::SMEM_BYTES, attr_done))
+        return SQ_ERR_CUDA;
+    const int active = active_clusters(kernel, 2, Cfg::SMEM_BYTES, sq::kPairThreads);
+    if (active <= 0)
+        return SQ_ERR_CUDA;
+    const int64_t tiles = ((M + sq::kPairBM - 1) / sq::kPairBM) * ((N + BN - 1) / BN);
+    if (tiles > INT_MAX / 2)
+        return SQ_ERR_UNSUPPORTED;
+    CUtensorMap ta, tsa, tb, tsb;
+    if (!make_tmap_mx4(&ta, xq, M, K, 128) || !make_tmap_scales(&tsa, sx, (M + 127) / 128, K, 1) ||
+        !make_tmap_mx4(&tb, wq, N, K, BN / 2) || !make_tmap_scales(&tsb, sw, (N + 127) / 128, K, Cfg::RT_B))
+        return SQ_ERR_CUDA;
+    const int64_t pairs = std::min<int64_t>(tiles, active);
+    if (debug_plan())
+        std::fprintf(stderr, "sq mx4 pair M=%lld N=%lld K=%lld: BN=%d stages=%d tiles=%lld pairs=%lld\n", (long long)M,
+                     (long long)N, (long long)K, BN, Cfg::STAGES, (long long)tiles, (long long)pairs);
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(sq::kPairThreads), Cfg::SMEM_BYTES, st, 2,
+                         1, ta, tsa, tb, tsb, y, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 8);
+}
+
+template <int OUT>
+sq_status launch_mx4_pair(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M,
+                          int64_t N, int64_t K, void *y, cudaStream_t st)
+{
+    static const int force = std::getenv("SQ_MX4_BN") ? std::atoi(std::getenv("SQ_MX4_BN")) : 0;
+    const int bn = force ? force : 192;
+    if (bn == 256)
+        return launch_mx4_pair_cfg<256, OUT>(xq, sx, wq, sw, M, N, K, y, st);
+    if (bn == 192)
+        return launch_mx4_pair_cfg<192, OUT>(xq, sx, wq, sw, M, N, K, y, st);
+    return launch_mx4_pair_cfg<128, OUT>(xq, sx, wq, sw, M, N, K, y, st);
+}
+
+// cnt: the tile counters, cleared by the kernel right before on the stream
+template <int OUT>
+sq_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M,
+                          int64_t N, int64_t K, void *y, int *cnt, float *slots, cudaStream_t st)
+{
+    if (M > sq::kMx4MaxTokens)
+        return launch_mx4_pair<OUT>(xq, sx, wq, sw, M, N, K, y, st);
+    switch (mx4_bnx(M)) {
+    case 32: return launch_mx4_stream<32, OUT>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st);
+    case 64: return launch_mx4_stream<64, OUT>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st);
+    default: return launch_mx4_stream<128, OUT>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st);
+    }
+}
+
+sq_status check_mx4_gemm_dims(int64_t M, int64_t N, int64_t K)
+{
+    if (!mx4_dims(M, K) || N < 16 || N % 16 != 0)
+        return SQ_ERR_INVALID_ARG;
+    if (M > kMx4MaxDim || N > kMx4MaxDim || K > kMx4MaxDim)
+        return SQ_ERR_UNSUPPORTED;
+    return SQ_OK;
+}
+
+__global__ void mx4_clear_kernel(int *p, int n)
+{
+    sq::pdl_prologue();
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x)
+        p[i] = 0;
+}
+
+// Workspace of sq_mx4_linear: codes and scales of x, then the product's.
+struct Mx4LinearWs {
+    size_t sx = 0;
+    Mx4Ws g;
+};
+
+inline Mx4LinearWs mx4_linear_ws(int64_t M, int64_t N, int64_t K)
+{
+    Mx4LinearWs w;
+    w.sx = round256(static_cast<size_t>(M) * static_cast<size_t>(K / 2));
+    w.g = mx4_ws(M, N, w.sx + scale_bytes(M, K));
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sq_mx4_scale_size(int64_t rows, int64_t K) { return mx4_dims(rows, K) ? scale_bytes(rows, K) : 0; }
+
+sq_status sq_mx4_quant_act(const void *x, sq_dtype dt, int64_t M, int64_t K, const float *s, uint8_t *xq, uint8_t *sx,
+                           sq_stream_t stream)
+{
+    const sq_status r = check_mx4_quant(x, dt, M, K, s, xq, sx);
+    return r != SQ_OK ? r : mx4_quant(x, dt, M, K, s, sq::MX4_OVER, xq, sx, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sq_status sq_mx4_quant_weight(const void *w, sq_dtype dt, int64_t N, int64_t K, const float *s, uint8_t *wq,
+                              uint8_t *sw, sq_stream_t stream)
+{
+    const sq_status r = check_mx4_quant(w, dt, N, K, s, wq, sw);
+    return r != SQ_OK ? r : mx4_quant(w, dt, N, K, s, sq::MX4_TIMES, wq, sw, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sq_status sq_mx4_dequant(const uint8_t *q, const uint8_t *sc, int64_t rows, int64_t K, void *out, sq_dtype out_dt,
+                         sq_stream_t stream)
+{
+    const sq_status r = check_mx4_quant(out, out_dt, rows, K, nullptr, q, sc);
+    if (r != SQ_OK)
+        return r;
+    DeviceInfo di;
+    if (!device_info(di))
+        return SQ_ERR_CUDA;
+    const Mx4Walk w = mx4_walk(rows, K, di.sms);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (out_dt == SQ_BF16)
+        return launch_kernel(sq::mx4_dequant_kernel<__nv_bfloat16>, dim3(w.gx, w.gy), dim3(sq::kMx4Threads), 0, st, 0, 0,
+                             q, sc, rows, K, static_cast<__nv_bfloat16 *>(out), w.log2tx, w.band);
+    return launch_kernel(sq::mx4_dequant_kernel<float>, dim3(w.gx, w.gy), dim3(sq::kMx4Threads), 0, st, 0, 0, q, sc,
+                         rows, K, static_cast<float *>(out), w.log2tx, w.band);
+}
+
+size_t sq_mx4_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    return check_mx4_gemm_dims(M, N, K) == SQ_OK ? mx4_ws(M, N, 0).total : 0;
+}
+
+sq_status sq_mx4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M, int64_t N,
+                      int64_t K, void *y, sq_dtype out_dt, void *workspace, size_t ws_bytes, sq_stream_t stream)
+{
+    if (!ok_ptr(xq) || !ok_ptr(sx) || !ok_ptr(wq) || !ok_ptr(sw) || !ok_ptr(y) || !valid_dtype(out_dt))
+        return SQ_ERR_INVALID_ARG;
+    sq_status r = check_mx4_gemm_dims(M, N, K);
+    if (r != SQ_OK)
+        return r;
+    const Mx4Ws w = mx4_ws(M, N, 0);
+    if (w.total > 0 && (!ok_ptr(workspace) || ws_bytes < w.total))
+        return SQ_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int *cnt = nullptr;
+    float *slots = nullptr;
+    if (w.total > 0) {
+        cnt = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + w.cnt);
+        slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.slots);
+        r = launch_kernel(mx4_clear_kernel, dim3(1), dim3(256), 0, st, 0, 0, cnt, w.ncnt);
+        if (r != SQ_OK)
+            return r;
+    }
+    return out_dt == SQ_BF16 ? launch_mx4_gemm<OUT_BF16>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st)
+                             : launch_mx4_gemm<OUT_F32>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st);
+}
+
+size_t sq_mx4_linear_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    return check_mx4_gemm_dims(M, N, K) == SQ_OK ? mx4_linear_ws(M, N, K).g.total : 0;
+}
+
+sq_status sq_mx4_linear(const void *x, sq_dtype in_dt, const float *s, const uint8_t *wq, const uint8_t *sw, int64_t M,
+                        int64_t N, int64_t K, void *y, sq_dtype out_dt, void *workspace, size_t ws_bytes,
+                        sq_stream_t stream)
+{
+    if (!ok_ptr(x) || !valid_dtype(in_dt) || !aligned16(s) || !ok_ptr(wq) || !ok_ptr(sw) || !ok_ptr(y) ||
+        !valid_dtype(out_dt))
+        return SQ_ERR_INVALID_ARG;
+    sq_status r = check_mx4_gemm_dims(M, N, K);
+    if (r != SQ_OK)
+        return r;
+    const Mx4LinearWs L = mx4_linear_ws(M, N, K);
+    if (!ok_ptr(workspace) || ws_bytes < L.g.total)
+        return SQ_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *xq = static_cast<uint8_t *>(workspace), *sx = xq + L.sx;
+    const bool few = L.g.ncnt > 0;
+    int *cnt = few ? reinterpret_cast<int *>(xq + L.g.cnt) : nullptr;
+    float *slots = few ? reinterpret_cast<float *>(xq + L.g.slots) : nullptr;
+    r = mx4_quant(x, in_dt, M, K, s, sq::MX4_OVER, xq, sx, st, cnt, L.g.ncnt);
+    if (r != SQ_OK)
+        return r;
+    return out_dt == SQ_BF16 ? launch_mx4_gemm<OUT_BF16>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st)
+                             : launch_mx4_gemm<OUT_F32>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st);
+}
+
+}  // extern "C"

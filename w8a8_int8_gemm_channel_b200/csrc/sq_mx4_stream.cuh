@@ -1,0 +1,476 @@
+// sq_mx4_stream.cuh -- the microscaled 4-bit product for few tokens (at most
+// 128): a stream over the weight, split evenly over every SM.
+//
+//   linear  y[m, n] = sum_k x[m, k] w[n, k]
+//   experts y[m, n] = sum_g v[g, m] sum_k h[g, m, k] w[e_g, n, k]
+//
+// (x, h, w the values that codes and scales stand for; e_g the g-th expert that
+// any token chose, v[g, m] token m's routing weight for it.)
+//
+// The tensor cores take the codes as they are (tcgen05.mma kind::mxf4) and
+// apply the scales of both sides to every 32 values of K, so nothing is
+// unpacked; the product accumulates in fp32.  The weight takes the 128-row MMA
+// side (a tile = 128 output channels), the tokens its N (BNX padded rows).  A
+// unit is one 128-byte k block (256 values) of one tile: 16 KB of codes and
+// 1 KB of scales.  The units, tile by tile (and within a tile expert by
+// expert), are cut into equal contiguous ranges, one per CTA and one CTA per
+// SM: the bound is the weight's bytes, and every SM streams the same number of
+// them whatever N, K and the experts are.  A tile that several CTAs share is
+// summed through the workspace: each contributor writes its fp32 partial and
+// counts itself in, and the one that completes the count adds the partials in
+// the contributors' order, so the sum's order is fixed by the sizes alone.
+//
+// Scales.  A stage's scale tiles go from shared memory to TMEM columns that
+// belong to the stage (tcgen05.cp), so they are rewritten only after the
+// commit that freed the stage.
+//
+// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM and MMA issue, warps
+// 2..5 epilogue.  Two accumulators, so a range's next tile (or expert)
+// accumulates while the epilogue drains one.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "sq_decode.cuh"
+#include "sq_mx4.cuh"
+#include "sq_ptx.cuh"
+
+namespace sq {
+
+constexpr int kMx4KB = 256;          // values of K a stage holds (128 bytes of codes a row)
+constexpr int kMx4MaxTokens = 128;   // of the streaming kernels
+constexpr int kMx4MaxSlots = 1024;   // tokens x choices of the experts layer
+constexpr int kMx4MaxExperts = 1024;
+constexpr unsigned int kErrWaitMx4 = 0xC00;
+
+template <int BNX>
+struct Mx4StreamCfg {
+    static constexpr int W_BYTES = 128 * 128;
+    static constexpr int X_BYTES = BNX * 128;
+    static constexpr int S_BYTES = 2 * kMx4TileBytes;  // scale tiles of one operand's stage
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * S_BYTES;
+    static constexpr int MAX_STAGES = BNX == 128 ? 6 : 8;
+    static constexpr int TMEM_COLS = pow2_at_least(2 * BNX + 16 * MAX_STAGES, 32);
+    static_assert(TMEM_COLS <= 512, "TMEM");
+};
+
+// ring, barriers (full, empty, tfull[2], tempty[2], drain), TMEM slot and two
+// flags, routing weights of a group [128] and its mask [4], expert mask and list
+__host__ __device__ constexpr int mx4_stream_smem(int stage_bytes, int stages, bool moe)
+{
+    return 1024 + stages * stage_bytes + (2 * stages + 5) * 8 + 24 +
+           (moe ? 2 * 512 + 2 * 16 + (kMx4MaxExperts / 32) * 4 + kMx4MaxExperts * 2 : 0);
+}
+
+// The experts that any of the S choices names, ascending, into `list`; returns
+// their number.  Choices outside [0, E) name none.  All `threads` threads call
+// it (it ends with a barrier of the whole block).
+__device__ __forceinline__ int mx4_active_experts(const int *__restrict__ ids, int S, int E, uint32_t *mask,
+                                                  uint16_t *list, volatile int *count)
+{
+    for (int i = threadIdx.x; i < kMx4MaxExperts / 32; i += blockDim.x)
+        mask[i] = 0u;
+    __syncthreads();
+    for (int i = threadIdx.x; i < S; i += blockDim.x) {
+        const int e = __ldg(ids + i);
+        if (e >= 0 && e < E)
+            atomicOr(mask + (e >> 5), 1u << (e & 31));
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        uint32_t m = mask[lane];
+        int n = __popc(m), before = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+            if (lane >= d)
+                before += o;
+        }
+        if (lane == 31)
+            *count = before;
+        before -= n;
+        while (m) {
+            list[before++] = static_cast<uint16_t>(lane * 32 + __ffs(m) - 1);
+            m &= m - 1;
+        }
+    }
+    __syncthreads();
+    return *count;
+}
+
+// MMAs of one stage: the scale tiles into the stage's TMEM columns, then one
+// instruction per 64 values of K.  `atoms` scale tiles (128 values each) and
+// `steps` instructions are inside K.
+template <int N>
+__device__ __forceinline__ void mx4_stage_mma(uint32_t d, uint32_t a0, uint32_t b0, uint32_t sa, uint32_t sb,
+                                              uint32_t ta, uint32_t tb, int steps, bool first, bool copy_b)
+{
+    tmem_cp_scales(ta, smem_desc_scales(sa));
+    if (copy_b)
+        tmem_cp_scales(tb, smem_desc_scales(sb));
+    if (steps > 2) {
+        tmem_cp_scales(ta + 4, smem_desc_scales(sa + kMx4TileBytes));
+        if (copy_b)
+            tmem_cp_scales(tb + 4, smem_desc_scales(sb + kMx4TileBytes));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < steps)
+            mma_mx4(d, smem_desc_k_sw128(a0 + 32 * k), smem_desc_k_sw128(b0 + 32 * k),
+                    (k & 1) ? idesc_mx4(128, N, 2) : idesc_mx4(128, N, 0), ta + 4 * (k >> 1), tb + 4 * (k >> 1),
+                    (first && k == 0) ? 0u : 1u);
+}
+
+// The weight side of a launch.  Linear: G = 1, one matrix.  Experts: the group
+// list is made in the kernel from ids.
+struct Mx4MoeArgs {
+    const int *ids;        // [T, topk]
+    const float *weights;  // [T, topk]
+    int topk, E;
+};
+
+template <int BNX, int OUT, bool MOE>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    mx4_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW,
+                      const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
+                      void *__restrict__ y, float *__restrict__ ws, int *__restrict__ cnt, int M, int N, int K,
+                      int ctas, int stages, int pre_wait, Mx4MoeArgs moe)
+{
+    using Cfg = Mx4StreamCfg<BNX>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool producer = warp == 0 && lane == 0;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gb = smem_raw + (base - raw);
+    const uint32_t sW = base;
+    const uint32_t sX = sW + stages * Cfg::W_BYTES;
+    const uint32_t sSW = sX + stages * Cfg::X_BYTES;
+    const uint32_t sSX = sSW + stages * Cfg::S_BYTES;
+    const uint32_t bars = sSX + stages * Cfg::S_BYTES;
+    auto full_bar = [&](int i) { return bars + 8u * i; };
+    auto empty_bar = [&](int i) { return bars + 8u * (stages + i); };
+    auto tfull_bar = [&](int b) { return bars + 8u * (2 * stages + b); };
+    auto tempty_bar = [&](int b) { return bars + 8u * (2 * stages + 2 + b); };
+    const uint32_t drain_bar = bars + 8u * (2 * stages + 4);
+    const uint32_t misc_off = (bars - base) + 8u * (2 * stages + 5);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gb + misc_off);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gb + misc_off + 4);
+    volatile int *last_flag = reinterpret_cast<volatile int *>(gb + misc_off + 8);
+    volatile int *n_groups = reinterpret_cast<volatile int *>(gb + misc_off + 12);
+    float *wt_s = reinterpret_cast<float *>(gb + misc_off + 24);             // [2][128]
+    uint32_t *wt_mask = reinterpret_cast<uint32_t *>(gb + misc_off + 24 + 1024);  // [2][4]
+    uint32_t *e_mask = wt_mask + 8;
+    uint16_t *e_list = reinterpret_cast<uint16_t *>(e_mask + kMx4MaxExperts / 32);
+
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(full_bar(i), 1);
+            mbar_init(empty_bar(i), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), 4);  // the 4 epilogue warps
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (producer) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmSW);
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmSX);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+
+    // With pre_wait the grid before is a kernel of this library that let this
+    // one start only after every earlier grid had completed: what that kernel
+    // does not write (the weight, the choices) may be read before the wait.
+    if (!pre_wait)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int G = 1;
+    if constexpr (MOE)
+        G = mx4_active_experts(moe.ids, M * moe.topk, moe.E, e_mask, e_list, n_groups);
+    if (pre_wait && !producer)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int T = (N + 127) / 128;
+    const int KB = (K + kMx4KB - 1) / kMx4KB;
+    const int64_t per_tile = static_cast<int64_t>(G) * KB;  // units of a tile
+    const int64_t U = T * per_tile;
+    const int64_t C = min(static_cast<int64_t>(ctas), U);  // CTAs with work
+    const int64_t c = blockIdx.x;
+    const bool works = c < C;
+    const int64_t u0 = works ? dec_start(c, U, C) : 0, u1 = works ? dec_start(c + 1, U, C) : 0;
+    const int64_t first_tile = works ? u0 / per_tile : 0;
+    auto steps_of = [&](int kb) { return min(4, (K - kb * kMx4KB + 63) >> 6); };
+
+    uint32_t issued_mask = 0, issued_parity = 0;
+    bool mma_issued_any = false;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // coordinates of unit u: k block, weight row, scale row tile, token row, token scale row tile
+            auto load_w = [&](int64_t u, int stage) {
+                const int64_t t = u / per_tile;
+                const int r = static_cast<int>(u - t * per_tile);
+                const int g = r / KB, kb = r - g * KB;
+                const int e = MOE ? e_list[g] : 0;
+                tma_load_2d(sW + stage * Cfg::W_BYTES, &tmW, full_bar(stage), kb * 128,
+                            e * N + static_cast<int>(t) * 128);
+                tma_load_3d(sSW + stage * Cfg::S_BYTES, &tmSW, full_bar(stage), 0, kb * 2, e * T + static_cast<int>(t));
+            };
+            auto load_x = [&](int64_t u, int stage) {
+                const int r = static_cast<int>(u % per_tile);
+                const int g = r / KB, kb = r - g * KB;
+                tma_load_2d(sX + stage * Cfg::X_BYTES, &tmX, full_bar(stage), kb * 128, MOE ? g * M : 0);
+                tma_load_3d(sSX + stage * Cfg::S_BYTES, &tmSX, full_bar(stage), 0, kb * 2, g);
+            };
+            const int64_t nu = u1 - u0;
+            const int pre = pre_wait ? static_cast<int>(nu < stages ? nu : stages) : 0;
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(full_bar(i), Cfg::STAGE_BYTES);
+                load_w(u0 + i, i);
+                issued_mask |= 1u << i;
+            }
+            if (pre_wait)
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (int i = 0; i < pre; ++i)
+                load_x(u0 + i, i);
+            int stage = pre % stages;
+            uint32_t phase = (pre == stages) ? 1u : 0u;
+            for (int64_t u = u0 + pre; u < u1; ++u) {
+                if (!bounded_wait(empty_bar(stage), phase ^ 1u, kErrWaitProducer, abort_flag))
+                    break;
+                mbar_arrive_expect_tx(full_bar(stage), Cfg::STAGE_BYTES);
+                load_w(u, stage);
+                load_x(u, stage);
+                issued_mask |= 1u << stage;
+                issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t tS = tmem_base + 2 * BNX;  // scales: 16 columns a stage
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int64_t u = u0; u < u1 && ok;) {
+                // one accumulator: the k blocks of one tile and expert
+                const int kb0 = static_cast<int>(u % KB);
+                const int kb1 = static_cast<int>(min(static_cast<int64_t>(KB), kb0 + (u1 - u)));
+                u += kb1 - kb0;
+                if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
+                    break;
+                tc_fence_after_sync();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BNX);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t t0 = tS + 16u * stage;
+                    mx4_stage_mma<BNX>(d, sW + stage * Cfg::W_BYTES, sX + stage * Cfg::X_BYTES,
+                                       sSW + stage * Cfg::S_BYTES, sSX + stage * Cfg::S_BYTES, t0, t0 + 8, steps_of(kb),
+                                       kb == kb0, true);
+                    mma_issued_any = true;
+                    mma_commit(empty_bar(stage));
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                mma_commit(tfull_bar(acc));
+                acc ^= 1;
+                if (acc == 0)
+                    acc_phase ^= 1u;
+            }
+        }
+    } else {
+        // epilogue warps 2..5: warp w reads TMEM lanes 32 (w % 4) .. +31
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;  // weight row within the tile
+        const int et = threadIdx.x - 64;      // 0..127
+        int acc = 0, wb = 0;
+        uint32_t acc_phase = 0;
+        auto store = [&](const float (&o)[BNX], int64_t n) {
+#pragma unroll
+            for (int j = 0; j < BNX; ++j)
+                if (j < M) {
+                    if constexpr (OUT == OUT_F32)
+                        reinterpret_cast<float *>(y)[static_cast<int64_t>(j) * N + n] = o[j];
+                    else
+                        reinterpret_cast<__nv_bfloat16 *>(y)[static_cast<int64_t>(j) * N + n] = __float2bfloat16_rn(o[j]);
+                }
+        };
+        if constexpr (MOE) {
+            if (U == 0) {  // no token chose an expert: zeros
+                const int64_t n = static_cast<int64_t>(M) * N;
+                for (int64_t i = c * 128 + et; i < n; i += static_cast<int64_t>(gridDim.x) * 128) {
+                    if constexpr (OUT == OUT_F32)
+                        reinterpret_cast<float *>(y)[i] = 0.0f;
+                    else
+                        reinterpret_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(0.0f);
+                }
+            }
+        }
+        for (int64_t u = u0; u < u1;) {
+            const int64_t t = u / per_tile;
+            const int64_t seg_begin = u;
+            const int64_t seg_end = min(u1, (t + 1) * per_tile);
+            const bool whole = seg_begin == t * per_tile && seg_end == (t + 1) * per_tile;
+            const int64_t n = t * 128 + row;
+            float o[BNX];
+#pragma unroll
+            for (int j = 0; j < BNX; ++j)
+                o[j] = 0.0f;
+            while (u < seg_end) {
+                const int r0 = static_cast<int>(u - t * per_tile);
+                const int g = r0 / KB, kb0 = r0 - g * KB;
+                u = min(seg_end, u + (KB - kb0));
+                if constexpr (MOE) {
+                    // this group's routing weights: thread i sums token i's
+                    // choices of the expert (two buffers, as the accumulators)
+                    const int e = e_list[g];
+                    float w = 0.0f;
+                    bool has = false;
+                    if (et < M)
+                        for (int k = 0; k < moe.topk; ++k)
+                            if (__ldg(moe.ids + et * moe.topk + k) == e) {
+                                w += __ldg(moe.weights + et * moe.topk + k);
+                                has = true;
+                            }
+                    wt_s[wb * 128 + et] = w;
+                    const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
+                    if (lane == 0)
+                        wt_mask[wb * 4 + (et >> 5)] = m;
+                    dec_bar_sync();
+                }
+                // a wait that gives up has set the error word and the abort
+                // flag: the warps go on (every later wait returns at once), so
+                // that their barriers stay matched
+                bounded_wait(tfull_bar(acc), acc_phase, kErrWaitAccFull, abort_flag);
+                __syncwarp();
+                tc_fence_after_sync();
+                const uint32_t lane_addr =
+                    tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BNX);
+#pragma unroll
+                for (int cc = 0; cc < BNX / 32; ++cc) {
+                    const uint32_t m = MOE ? wt_mask[wb * 4 + cc] : 0u;
+                    if (MOE ? m == 0u : cc * 32 >= M)
+                        continue;
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(lane_addr + cc * 32, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if constexpr (MOE) {
+                            if (m & (1u << j))
+                                o[cc * 32 + j] += wt_s[wb * 128 + cc * 32 + j] * __uint_as_float(r[j]);
+                        } else {
+                            o[cc * 32 + j] = __uint_as_float(r[j]);
+                        }
+                    }
+                }
+                wb ^= 1;
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(tempty_bar(acc));
+                acc ^= 1;
+                if (acc == 0)
+                    acc_phase ^= 1u;
+            }
+            if (whole) {
+                if (n < N)
+                    store(o, n);
+                continue;
+            }
+            // this range's part of a shared tile: 4 tokens x 128 rows at a time
+            const int nv = (M + 3) >> 2;
+            auto slot_of = [&](int64_t c2) {
+                return reinterpret_cast<float4 *>(ws) +
+                       (c2 * 2 + (dec_start(c2, U, C) / per_tile == t ? 0 : 1)) * (BNX / 4 * 128);
+            };
+            {
+                float4 *mine = reinterpret_cast<float4 *>(ws) + (c * 2 + (t == first_tile ? 0 : 1)) * (BNX / 4 * 128);
+#pragma unroll
+                for (int v = 0; v < BNX / 4; ++v)
+                    if (v < nv)
+                        mine[v * 128 + row] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            }
+            dec_bar_sync();
+            const int64_t cf = dec_owner(t * per_tile, U, C), cl = dec_owner((t + 1) * per_tile - 1, U, C);
+            if (et == 0) {
+                // release: this CTA's partial (ordered before it by the
+                // barrier) precedes the count; acquire: the others' partials
+                // precede the reads that follow
+                const int old = atom_add_acq_rel_gpu(cnt + t, 1);
+                *last_flag = old == static_cast<int>(cl - cf);
+            }
+            dec_bar_sync();
+            if (*last_flag) {
+#pragma unroll
+                for (int j = 0; j < BNX; ++j)
+                    o[j] = 0.0f;
+                for (int64_t c2 = cf; c2 <= cl; ++c2) {
+                    const float4 *p = slot_of(c2) + row;
+#pragma unroll
+                    for (int v = 0; v < BNX / 4; ++v)
+                        if (v < nv) {
+                            const float4 a = __ldcg(p + v * 128);
+                            o[4 * v] += a.x;
+                            o[4 * v + 1] += a.y;
+                            o[4 * v + 2] += a.z;
+                            o[4 * v + 3] += a.w;
+                        }
+                }
+                if (n < N)
+                    store(o, n);
+            }
+            dec_bar_sync();  // last_flag is rewritten by the next shared tile
+        }
+    }
+
+    // ---- teardown ------------------------------------------------------------
+    if (warp == 1 && lane == 0 && *abort_flag && mma_issued_any) {
+        mma_commit(drain_bar);
+        bounded_wait(drain_bar, 0, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
+    }
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        for (int i = 0; i < stages; ++i)
+            if (issued_mask & (1u << i))
+                bounded_wait(full_bar(i), (issued_parity >> i) & 1u, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+}  // namespace sq

@@ -13,9 +13,10 @@
 namespace sq {
 
 // ----------------------------------------------------------------------------
-// device error word (cleared and read by sq_device_status on the host)
+// device error word (cleared and read by sq_device_status on the host); each
+// translation unit has its own
 // ----------------------------------------------------------------------------
-__device__ unsigned int g_sq_device_error = 0;
+static __device__ unsigned int g_sq_device_error = 0;
 
 // Location codes written to the error word (first error wins).
 enum : unsigned int {
@@ -238,6 +239,18 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// 3-D tile load global -> shared (the scale tiles of the microscaled format:
+// x inside a 512-byte tile, y the tile along K, z the row tile).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // ----------------------------------------------------------------------------
 // packed fp32 pairs (sm_100): two independent IEEE round-to-nearest
 // operations per instruction, exactly the scalar _rn results (the toolkit's
@@ -440,9 +453,87 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// The same for a 3-D tile (scale tiles of the microscaled format).
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t x,
+                                                 int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// ----------------------------------------------------------------------------
+// Microscaled 4-bit MMA (kind::mxf4: E2M1 operands, one E8M0 scale per row and
+// 32 values of K, K = 64 an instruction, fp32 accumulator).  The scales are
+// read from TMEM: row r of a 128-row operand at lane r % 32 of every
+// 32-lane group, column r / 32, two of that word's four bytes an instruction
+// (the instruction descriptor's scale id 0 or 2).
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Across a CTA pair (M = 256): each CTA's TMEM holds the scales of its own 128
+// rows of A and of all N rows of B.
+__device__ __forceinline__ void mma_mx4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// One 512-byte scale tile (32 rows of 16 bytes in shared memory) into 4 TMEM
+// columns, the same 32 lanes repeated for all four lane groups.  Ordered
+// before the MMAs that this thread issues after it.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// The same in both CTAs of a pair, each from its own shared memory.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
 // ----------------------------------------------------------------------------
 // Descriptors
 // ----------------------------------------------------------------------------
+// Shared-memory descriptor of a scale tile: no swizzle, 8-row groups of 16-byte
+// rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(128u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    return d;
+}
+
+// Instruction descriptor for kind::mxf4, both operands E2M1 and K-major:
+//   bits 4-5 scale id of B, 7-9 A format (1 = E2M1), 10-11 B format (1 = E2M1),
+//   17-22 N >> 3, 23 scale type (1 = E8M0), 24-28 M >> 4, 29-30 scale id of A.
+__host__ __device__ constexpr uint32_t idesc_mx4(int M, int N, int scale_id)
+{
+    return (static_cast<uint32_t>(scale_id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(scale_id) << 29);
+}
+
 // Shared-memory matrix descriptor for a K-major operand stored with the
 // 128-byte swizzle (the layout a TMA load with CU_TENSOR_MAP_SWIZZLE_128B and
 // a 128-byte inner box writes): rows of 128 bytes, 8-row atoms of 1024 bytes.
