@@ -191,7 +191,7 @@ sq_status launch_mx4_pair_cfg(const uint8_t *xq, const uint8_t *sx, const uint8_
     static std::atomic<uint64_t> attr_done{0};
     if (!ensure_smem_attr(kernel, Cfg::SMEM_BYTES, attr_done))
         return SQ_ERR_CUDA;
-    const int active = active_clusters(kernel, 2, Cfg::SMEM_BYTES, sq::kPairThreads);
+    const int active = active_clusters(kernel, 2, Cfg::SMEM_BYTES, sq::kMx4PairThreads);
     if (active <= 0)
         return SQ_ERR_CUDA;
     const int64_t tiles = ((M + sq::kPairBM - 1) / sq::kPairBM) * ((N + BN - 1) / BN);
@@ -205,21 +205,44 @@ sq_status launch_mx4_pair_cfg(const uint8_t *xq, const uint8_t *sx, const uint8_
     if (debug_plan())
         std::fprintf(stderr, "sq mx4 pair M=%lld N=%lld K=%lld: BN=%d stages=%d tiles=%lld pairs=%lld\n", (long long)M,
                      (long long)N, (long long)K, BN, Cfg::STAGES, (long long)tiles, (long long)pairs);
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(sq::kPairThreads), Cfg::SMEM_BYTES, st, 2,
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(sq::kMx4PairThreads), Cfg::SMEM_BYTES, st, 2,
                          1, ta, tsa, tb, tsb, y, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 8);
+}
+
+// Tile width: the fewest rounds of tiles over the pairs, a round costing one
+// tile's time.  A tile's time is far from proportional to its width (an MMA of
+// N = 128 takes as long as one of 256): at 8192 x 8192 x 28672 a 256 / 192 /
+// 128-wide tile took 50.1 / 43.2 / 34.1 us, which gives the weights below.
+inline int pick_mx4_bn(int64_t M, int64_t N, int64_t pairs)
+{
+    constexpr int cand[3] = {256, 192, 128};
+    constexpr int64_t tile_time[3] = {100, 86, 68};
+    const int64_t mt = (M + sq::kPairBM - 1) / sq::kPairBM;
+    int best = 256;
+    int64_t best_cost = INT64_MAX;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = mt * ((N + cand[i] - 1) / cand[i]);
+        const int64_t cost = (tiles + pairs - 1) / pairs * tile_time[i];
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = cand[i];
+        }
+    }
+    return best;
 }
 
 template <int OUT>
 sq_status launch_mx4_pair(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M,
                           int64_t N, int64_t K, void *y, cudaStream_t st)
 {
-    static const int force = std::getenv("SQ_MX4_BN") ? std::atoi(std::getenv("SQ_MX4_BN")) : 0;
-    const int bn = force ? force : 192;
-    if (bn == 256)
-        return launch_mx4_pair_cfg<256, OUT>(xq, sx, wq, sw, M, N, K, y, st);
-    if (bn == 192)
-        return launch_mx4_pair_cfg<192, OUT>(xq, sx, wq, sw, M, N, K, y, st);
-    return launch_mx4_pair_cfg<128, OUT>(xq, sx, wq, sw, M, N, K, y, st);
+    DeviceInfo di;
+    if (!device_info(di))
+        return SQ_ERR_CUDA;
+    switch (pick_mx4_bn(M, N, std::max(di.sms / 2, 1))) {
+    case 256: return launch_mx4_pair_cfg<256, OUT>(xq, sx, wq, sw, M, N, K, y, st);
+    case 192: return launch_mx4_pair_cfg<192, OUT>(xq, sx, wq, sw, M, N, K, y, st);
+    default: return launch_mx4_pair_cfg<128, OUT>(xq, sx, wq, sw, M, N, K, y, st);
+    }
 }
 
 // cnt: the tile counters, cleared by the kernel right before on the stream

@@ -7,16 +7,21 @@
 // An output tile is 256 tokens x BN channels.  CTA r of a pair loads rows
 // [m0 + 128 r, +128) of x and rows [n0 + r BN/2, +BN/2) of w with plain TMA,
 // and the scale tiles of its own x rows and of all BN rows of w (each SM's
-// tensor core applies the scales of every column of its 128 rows).  The pair's
-// first CTA copies both CTAs' scale tiles into TMEM columns that belong to the
-// stage and issues the MMAs.  No scale is left for the epilogue: it rounds and
-// stores.
+// tensor core applies the scales of every column of its 128 rows).  In the
+// pair's first CTA one warp copies both CTAs' scale tiles into TMEM columns that
+// belong to the stage (tcgen05.cp) and another issues the MMAs.  Issued by the
+// MMA thread itself the copies and the MMAs took turns (8192 x 8192 x 28672: 1025
+// us against 755); from a warp of their own they run stages ahead.  No scale is
+// left for the epilogue: it rounds and stores.
 //
 // TMEM (512 columns): the accumulators and 8 + 16 columns of scales a stage.
-// BN = 192 and 128 fit two accumulators, so the epilogue of one tile overlaps
-// the main loop of the next.  BN = 256 (a quarter less operand traffic a
-// product than 192) fits one; its epilogue hands the columns back in eight
-// parts and the next tile's main loop starts when all are read.
+// BN = 192 and 128 fit two accumulators, 256 one.  The epilogue therefore first
+// takes the whole accumulator into registers (eight warps, half the columns
+// each) and frees it, and stores while the next tile multiplies.
+//
+// Bound: the 1 kW power cap.  8192 x 8192 x 28672 runs at 4.8 PFLOP/s held (1.40
+// GHz, tensor pipe 70% busy) and 5.5 in a burst; without its operand loads the
+// same loop makes 6.5 at 1.85 GHz, without the scale copies as well 8.3.
 #pragma once
 
 #include <cstdint>
@@ -28,6 +33,8 @@
 #include "sq_ptx.cuh"
 
 namespace sq {
+
+constexpr int kMx4PairThreads = 352;  // producer, MMA, scale copies, 8 epilogue warps
 
 template <int BN>
 struct Mx4PairCfg {
@@ -43,7 +50,7 @@ struct Mx4PairCfg {
     static constexpr int FIT_SMEM = (232448 - 1024 - 256) / STAGE_BYTES;
     static constexpr int STAGES = FIT_TMEM < FIT_SMEM ? FIT_TMEM : FIT_SMEM;
     static constexpr int TMEM_COLS = 512;
-    static constexpr int NUM_BARS = 2 * STAGES + 5;  // full, empty, tfull[2], tempty[2], drain
+    static constexpr int NUM_BARS = 3 * STAGES + 5;  // full, empty, tfull[2], tempty[2], drain, scales
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NUM_BARS * 8 + 16;
     static_assert(BN == 128 || BN == 192 || BN == 256, "tile width");
     static_assert(STAGES >= 4 && SMEM_BYTES <= 232448, "ring");
@@ -77,7 +84,7 @@ __device__ __forceinline__ void mx4_store_row(const uint32_t (&r)[32], int n0, i
 }
 
 template <int BN, int OUT>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kMx4PairThreads, 1)
     mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSA,
                     const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmSB,
                     void *__restrict__ y, int M, int N, int K, int group_m)
@@ -105,6 +112,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto tfull_bar = [&](int b) { return sBar + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](int b) { return sBar + 8u * (2 * STAGES + 2 + b); };
     const uint32_t drain_bar = sBar + 8u * (2 * STAGES + 4);
+    auto scale_bar = [&](int s) { return sBar + 8u * (2 * STAGES + 5 + s); };
     const uint32_t slot_off = (sBar - base) + 8u * Cfg::NUM_BARS;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + slot_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + slot_off + 4);
@@ -119,10 +127,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(scale_bar(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 8);  // 4 epilogue warps in each CTA
+            mbar_init(tempty_bar(b), 16);  // 8 epilogue warps in each CTA
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -185,8 +194,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     ok = bounded_wait(empty_bar(s), (issued_parity >> s) & 1u, kErrWaitDrain, abort_flag);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const uint32_t leader = elect_one();
             const uint32_t tS = tmem_base + Cfg::NACC * BN;
+            auto steps_of = [&](int kb) { return min(4, (K - kb * kMx4KB + 63) >> 6); };
+            const uint64_t a_desc = smem_desc_k_sw128(sA), b_desc = smem_desc_k_sw128(sB);  // + 2 a 32-byte step
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;
@@ -203,54 +215,89 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 // starts that many columns in, 32 rows a column
                 const uint32_t shift = static_cast<uint32_t>(n_blk * BN % 128 / 32);
                 for (int kb = 0; kb < k_blocks; ++kb) {
-                    if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                    const int next = stage + 1 == STAGES ? 0 : stage + 1;
+                    if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
+                        !bounded_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t a0 = sA + stage * Cfg::A_BYTES;
-                    const uint32_t b0 = sB + stage * Cfg::B_BYTES;
+                    const uint64_t a0 = a_desc + static_cast<uint32_t>(stage * (Cfg::A_BYTES >> 4));
+                    const uint64_t b0 = b_desc + static_cast<uint32_t>(stage * (Cfg::B_BYTES >> 4));
                     const uint32_t ta = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage), tb = ta + 8;
-                    const int steps = min(4, (K - kb * kMx4KB + 63) >> 6);
-                    // the scale tiles in TMEM: x [k tile], w [k tile][row tile], 4 columns each
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (2 * i >= steps)
-                            break;
-                        tmem_cp_scales_pair(ta + 4 * i,
-                                            smem_desc_scales(sSA + stage * Cfg::SA_BYTES + i * kMx4TileBytes));
-#pragma unroll
-                        for (int rt = 0; rt < Cfg::RT_B; ++rt)
-                            tmem_cp_scales_pair(tb + 4 * (i * Cfg::RT_B + rt),
-                                                smem_desc_scales(sSB + stage * Cfg::SB_BYTES +
-                                                                 (rt * 2 + i) * kMx4TileBytes));
-                    }
+                    const int steps = steps_of(kb);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (k < steps)
-                            mma_mx4_pair(d, smem_desc_k_sw128(a0 + 32 * k), smem_desc_k_sw128(b0 + 32 * k),
+                            mma_mx4_pair_warp(leader, d, a0 + 2 * k, b0 + 2 * k,
                                          (k & 1) ? idesc_mx4(kPairBM, BN, 2) : idesc_mx4(kPairBM, BN, 0),
                                          ta + 4 * (k >> 1), tb + 4 * Cfg::RT_B * (k >> 1) + shift,
                                          (kb > 0 || k != 0) ? 1u : 0u);
                     mma_issued_any = true;
-                    mma_commit_pair(empty_bar(stage), 0x3);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    mma_commit_pair_warp(leader, empty_bar(stage), 0x3);
+                    stage = next;
+                    phase ^= next == 0 ? 1u : 0u;
                 }
                 if (!ok)
                     break;
-                mma_commit_pair(tfull_bar(acc), 0x3);
+                mma_commit_pair_warp(leader, tfull_bar(acc), 0x3);
                 if (++acc == Cfg::NACC) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
         }
+    } else if (warp == 2) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t tS = tmem_base + Cfg::NACC * BN;
+            auto steps_of = [&](int kb) { return min(4, (K - kb * kMx4KB + 63) >> 6); };
+            // scale tiles of a filled stage into its TMEM columns: x [k tile],
+            // w [k tile][row tile], 4 columns each
+            auto copy_scales = [&](int stage, int steps) {
+                const uint32_t ta = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage), tb = ta + 8;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (2 * i >= steps)
+                        break;
+                    tmem_cp_scales_pair(ta + 4 * i, smem_desc_scales(sSA + stage * Cfg::SA_BYTES + i * kMx4TileBytes));
+#pragma unroll
+                    for (int rt = 0; rt < Cfg::RT_B; ++rt)
+                        tmem_cp_scales_pair(tb + 4 * (i * Cfg::RT_B + rt),
+                                            smem_desc_scales(sSB + stage * Cfg::SB_BYTES + (rt * 2 + i) * kMx4TileBytes));
+                }
+            };
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            int last = -1;
+            uint32_t last_phase = 0;
+            for (int t = pair; t < tiles && ok; t += pairs)
+                for (int kb = 0; kb < k_blocks; ++kb) {
+                    if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    copy_scales(stage, steps_of(kb));
+                    mma_commit_pair_local(scale_bar(stage));
+                    last = stage;
+                    last_phase = phase;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            // the last copies have landed before the CTA may release TMEM
+            if (last >= 0)
+                bounded_wait(scale_bar(last), last_phase, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
+        }
     } else {
-        // epilogue warps 2..5: warp w reads TMEM lanes 32 (w % 4) .. +31
+        // epilogue warps 3..10: warp w reads TMEM lanes 32 (w % 4) .. +31, half
+        // of the tile's columns, all into registers; then the accumulator is
+        // free for the next tile while the stores run
+        constexpr int NC = BN / 64;  // chunks of 32 columns a warp
         const int quarter = warp & 3;
+        const int half = (warp - 3) >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t tempty_first = map_shared_rank(tempty_bar(0), 0);
         int acc = 0;
@@ -263,20 +310,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 break;
             tc_fence_after_sync();
             const int64_t m = static_cast<int64_t>(m_blk) * kPairBM + rank * 128 + row;
-            const uint32_t tbase =
-                tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN);
-#pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
-                const int n0 = n_blk * BN + c * 32;
-                if (n0 >= N)
-                    break;
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tbase + c * 32, r);
-                tmem_ld_wait();
-                if (m < M)
-                    mx4_store_row<OUT>(r, n0, N, y, m);
-                __syncwarp();
-            }
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                   static_cast<uint32_t>(acc * BN + half * (BN / 2));
+            uint32_t r[NC][32];
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                tmem_ld_32x32b_x32(tbase + c * 32, r[c]);
+            tmem_ld_wait();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
@@ -285,13 +325,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 acc = 0;
                 acc_phase ^= 1u;
             }
+            if (m < M) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const int n0 = n_blk * BN + half * (BN / 2) + c * 32;
+                    if (n0 < N)
+                        mx4_store_row<OUT>(r[c], n0, N, y, m);
+                }
+            }
+            __syncwarp();
         }
     }
 
     // ---- teardown ----------------------------------------------------------
-    if (warp == 1 && lane == 0 && rank == 0 && *abort_flag && mma_issued_any) {
+    if (warp == 1 && rank == 0 && *abort_flag && mma_issued_any) {
         // every MMA of the pair finishes before either CTA releases TMEM
-        mma_commit_pair_local(drain_bar);
+        // (by the lane that issued them)
+        __syncwarp();
+        if (elect_one())
+            mma_commit_pair_local(drain_bar);
+        __syncwarp();
         bounded_wait(drain_bar, 0, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
     }
     if (warp == 0 && lane == 0 && rank == 0 && *abort_flag) {

@@ -497,6 +497,46 @@ __device__ __forceinline__ void mma_mx4_pair(uint32_t d_tmem, uint64_t adesc, ui
         : "memory");
 }
 
+// The pair MMA and its commit for a whole converged warp: the lane whose
+// `leader` is not 0 issues.  With the branch inside the instruction the operands
+// stay warp-uniform; under an `if (lane == 0)` each is moved to a uniform
+// register first, which takes longer than the MMA itself.
+__device__ __forceinline__ void mma_mx4_pair_warp(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                  uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_pair_warp(uint32_t leader, uint32_t bar, uint16_t cta_mask)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            bar),
+        "h"(cta_mask), "r"(leader)
+        : "memory");
+}
+
+// 1 in one lane of the converged warp, 0 in the others
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(v));
+    return v;
+}
+
 // One 512-byte scale tile (32 rows of 16 bytes in shared memory) into 4 TMEM
 // columns, the same 32 lanes repeated for all four lane groups.  Ordered
 // before the MMAs that this thread issues after it.
