@@ -438,6 +438,65 @@ SQ_API sq_status sq_mx4_linear(const void *x, sq_dtype in_dt, const float *s, co
                                size_t ws_bytes, sq_stream_t stream);
 
 /*
+ * A whole layer of experts for a few tokens on MXFP4 weights, in two kernels:
+ *   h[e, t, j] = silu(sum_k x[t, k] wg[e, j, k]) * sum_k x[t, k] wu[e, j, k]
+ *                (fp32; silu(v) = v / (1 + e^-v)), quantised to MXFP4 along j
+ *   y[t, n]    = sum_i weights[t, i] * sum_j h[ids[t, i], t, j] wd[ids[t, i], n, j]
+ * with fp32 accumulation and one rounding to out_dt.
+ *   xq, sx   the tokens [T, H] as MXFP4 codes and scale tiles (from
+ *            sq_mx4_quant_act or sq_residual_norm_quant_mx4).
+ *   ids      [T, topk] int32, the experts a token chose, in any order.  A choice
+ *            outside [0, E) counts for nothing (an expert that lives elsewhere,
+ *            padding): a token without any gets a row of zeros.  An expert that a
+ *            token names twice counts with both weights.
+ *   weights  [T, topk] fp32.
+ *   wg, wu   [E, I, H / 2] codes of the gate and up projections; sg, su their
+ *            scale tiles, sq_mx4_scale_size(I, H) bytes an expert.
+ *   wd       [E, H, I / 2] codes of the down projection; sd its scale tiles,
+ *            sq_mx4_scale_size(H, I) bytes an expert.
+ *   y        [T, H] dtype out_dt.
+ *   workspace: as in sq_mx4_gemm, at least sq_mx4_moe_workspace_size bytes.
+ * Only the experts that some token chose are read.  H and I are multiples of 32;
+ * T at most 128, T * topk and E at most 1024, E * max(H, I) at most 2^30
+ * (SQ_ERR_UNSUPPORTED).  The order of the sums is fixed by the sizes, the
+ * device and the set of chosen experts.
+ */
+SQ_API size_t sq_mx4_moe_workspace_size(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I);
+SQ_API sq_status sq_mx4_moe(const uint8_t *xq, const uint8_t *sx, const int32_t *ids, const float *weights, int64_t T,
+                            int64_t topk, int64_t E, int64_t H, int64_t I, const uint8_t *wg, const uint8_t *sg,
+                            const uint8_t *wu, const uint8_t *su, const uint8_t *wd, const uint8_t *sd, void *y,
+                            sq_dtype out_dt, void *workspace, size_t ws_bytes, sq_stream_t stream);
+
+/*
+ * The norms on both sides of a residual addition with the block's gate and
+ * residual scale, fused with the next linear's quantiser (one pass over the
+ * tokens instead of four):
+ *   n  = (b * rb) * gamma     rb = RN(1 / sqrt(mean(b^2) + eps)); n = b when gamma is NULL
+ *   u  = n * gate             u = n when gate is NULL
+ *   r' = r + u * c            rounded to dt and stored in r_out
+ *   a  = (r' * ra) * g        ra = RN(1 / sqrt(mean(r'^2) + eps)), r' as stored
+ * each product and sum one fp32 operation; the mean squares as in
+ * sq_rmsnorm_quant (fp64 sums of exact squares, order unspecified; 1 / sqrt of
+ * 0 is 0).  a is then quantised
+ *   sq_residual_norm_quant:     as in sq_quant_act, xq [M, K] int8 and sx [M]
+ *                               (inputs finite, as there)
+ *   sq_residual_norm_quant_mx4: as in sq_mx4_quant_act without factors, codes
+ *                               [M, K / 2] and scale tiles
+ *   b, r [M, K] dtype dt: the block's output and the residual stream; r_out
+ *   [M, K] dt, r itself allowed (in place), not b.  gamma [K] fp32 or NULL;
+ *   gate [ceil(M / gate_tokens), K] dt or NULL, row m / gate_tokens for token m
+ *   (gate_tokens >= M: one gate for all); c finite; g [K] fp32 (sq_fold_gamma
+ *   folds the next linear's factors in); eps >= 0 finite.
+ * K a multiple of 16 (32 for MXFP4), at most 32768 (bf16) or 16384 (fp32).
+ */
+SQ_API sq_status sq_residual_norm_quant(const void *b, sq_dtype dt, int64_t M, int64_t K, const float *gamma,
+                                        const void *gate, int64_t gate_tokens, float c, const void *r, void *r_out,
+                                        const float *g, float eps, int8_t *xq, float *sx, sq_stream_t stream);
+SQ_API sq_status sq_residual_norm_quant_mx4(const void *b, sq_dtype dt, int64_t M, int64_t K, const float *gamma,
+                                            const void *gate, int64_t gate_tokens, float c, const void *r, void *r_out,
+                                            const float *g, float eps, uint8_t *xq, uint8_t *sx, sq_stream_t stream);
+
+/*
  * Device error word: synchronises `stream`, then reads and clears the error
  * word the kernels set when a bounded on-chip wait gives up, or when
  * sq_gptq_factor meets a non-positive pivot.  Returns SQ_OK, SQ_ERR_TIMEOUT

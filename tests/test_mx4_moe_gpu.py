@@ -1,0 +1,153 @@
+"""The experts layer for few tokens on MXFP4 weights (sq_mx4_moe) against its
+definition in 64 bits, with tolerances from arithmetic.
+
+The quantised h between the two halves is the one step that is not continuous:
+a value of h that the fp32 product puts on the other side of a rounding border
+gives another code.  The gate and up products are off by at most
+K 2^-23 of their sums of magnitudes (oracle/mx4.py), so h by a known amount d;
+a code can differ only where a border lies within d, and then by one step (a
+sixth of the block's top binade or less is excluded: the step above 4 is 2
+units).  The bound on y is the sum of those steps over the down product, plus
+the product's own rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import w8a8_int8_gemm_channel_b200 as sq
+from oracle import mx4
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from w8a8_int8_gemm_channel_b200 import _build
+
+    _build.build()
+    yield
+    st, code = sq.sq_device_status()
+    assert st == sq.SQ_OK, f"device error word {code:#x}"
+
+
+def make(T, topk, E, H, I, seed):
+    rng = np.random.default_rng(seed)
+    x = mx4.quantize(rng.standard_normal((T, H)) * np.where(rng.random(H) < 0.01, 30.0, 1.0))
+    w = {k: [mx4.quantize(rng.standard_normal(shape) * 0.05) for _ in range(E)]
+         for k, shape in (("g", (I, H)), ("u", (I, H)), ("d", (H, I)))}
+    ids = np.stack([rng.permutation(E)[:topk] if topk <= E else rng.integers(0, E, topk) for _ in range(T)]).astype(np.int32)
+    return x, w, ids, rng.random((T, topk)).astype(np.float32)
+
+
+def silu(v):
+    return v / (1 + np.exp(-v))
+
+
+def definition(x, w, ids, weights, out_eps):
+    """(y, bound) of the layer in 64 bits."""
+    T, topk = ids.shape
+    H, I = x[2].shape[1], w["g"][0][2].shape[0]
+    y, bound = np.zeros((T, H)), np.zeros((T, H))
+    for e in sorted(set(ids[(ids >= 0) & (ids < len(w["g"]))].tolist())):
+        rows = np.flatnonzero((ids == e).any(1))
+        v = np.where(ids[rows] == e, weights[rows].astype(np.float64), 0.0).sum(1)[:, None]
+        xv = x[2][rows]
+        (g, gm), (u, um) = mx4.product(xv, w["g"][e][2]), mx4.product(xv, w["u"][e][2])
+        dg, du = mx4.product_bound(H, gm, g, 0.0), mx4.product_bound(H, um, u, 0.0)
+        h = silu(g) * u
+        # |silu'| <= 1.1; e^x, the division and the products round by a few 2^-24
+        dh = 1.1 * dg * np.abs(u) + np.abs(silu(g)) * du + 1.1 * dg * du + 2.0 ** -21 * np.abs(h)
+        _, _, hv = mx4.quantize(h)
+        lo, hi = mx4.quantize(np.abs(h) - np.minimum(dh, np.abs(h)))[2], mx4.quantize(np.abs(h) + dh)[2]
+        # a block whose top crosses a power of two may take the scale next to it: its codes move by a step of that scale
+        top, dt = np.abs(h).reshape(len(rows), -1, 32).max(-1), dh.reshape(len(rows), -1, 32).max(-1)
+        crosses = np.frexp(top - np.minimum(dt, top * 0.5))[1] != np.frexp(top + dt)[1]
+        step = np.maximum(np.abs(hi - np.abs(hv)), np.abs(lo - np.abs(hv)))
+        step = np.where(np.repeat(crosses, 32, 1), np.abs(h) * 0.5 + np.repeat(top, 32, 1) / 4, step)
+        out, om = mx4.product(hv, w["d"][e][2])
+        y[rows] += v * out
+        wd = np.abs(w["d"][e][2]).T
+        bound[rows] += np.abs(v) * (step @ wd + mx4.product_bound(I, om + step @ wd, out, 0.0)) + 2.0 ** -22 * topk * np.abs(v * out)
+    return y, bound + out_eps / 2 * np.abs(y) + 2.0 ** -126
+
+
+def on_gpu(x, w, ids, weights):
+    cuda = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    t = [cuda(x[0]), cuda(x[1]), cuda(ids), cuda(weights)]
+    for k in ("g", "u", "d"):
+        t += [cuda(np.stack([q[0] for q in w[k]])), cuda(np.stack([q[1] for q in w[k]]))]
+    return t
+
+
+def check(y, want, bound):
+    off = np.abs(y.double().cpu().numpy() - want)
+    assert np.isfinite(y.double().cpu().numpy()).all()
+    assert (off <= bound).all(), f"off by {(off / bound).max():.3g} times the bound"
+
+
+@pytest.mark.parametrize("T,topk,E,H,I", [(1, 1, 1, 32, 32), (1, 2, 8, 256, 128), (3, 2, 4, 96, 160), (17, 4, 16, 544, 416),
+                                          (33, 2, 6, 288, 96), (64, 6, 32, 512, 288), (65, 3, 5, 160, 640),
+                                          (128, 8, 40, 256, 224), (128, 1, 3, 1056, 64), (5, 8, 4, 128, 96), (2, 2, 64, 2048, 1408)])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_layer(T, topk, E, H, I, out):
+    case = make(T, topk, E, H, I, T + H)
+    want, bound = definition(*case, torch.finfo(out).eps)
+    t = on_gpu(*case)
+    ws = torch.full((sq.sq_mx4_moe_workspace_size(T, topk, E, H, I),), 0xFF, dtype=torch.uint8, device="cuda")
+    y = torch.full((T + 1, H), 9.0, dtype=out, device="cuda")
+    for _ in range(2):
+        sq.sq_mx4_moe(*t, y[:T], ws)
+        check(y[:T], want, bound)
+    assert (y[T] == 9.0).all()
+    first = y.clone()
+    ws.fill_(0x7F)
+    sq.sq_mx4_moe(*t, y[:T], ws)
+    assert torch.equal(first, y)  # nothing hangs on the workspace's contents
+
+
+def test_choices_that_name_no_expert():
+    """-1, E and far values count for nothing; a token without any expert gets zeros; all tokens so: all zeros."""
+    T, topk, E, H, I = 9, 3, 6, 256, 160
+    x, w, ids, weights = make(T, topk, E, H, I, 3)
+    ids[0] = -1
+    ids[1] = [E, 2 ** 31 - 1, -(2 ** 31)]
+    ids[2, 1] = -1
+    want, bound = definition(x, w, ids, weights, torch.finfo(F32).eps)
+    y = torch.empty(T, H, device="cuda")
+    sq.sq_mx4_moe(*on_gpu(x, w, ids, weights), y)
+    check(y, want, bound)
+    assert (y[:2] == 0).all()
+    for out in (F32, BF16):
+        y = torch.full((T, H), 5.0, dtype=out, device="cuda")
+        sq.sq_mx4_moe(*on_gpu(x, w, np.full_like(ids, -1), weights), y)
+        assert (y == 0).all()
+
+
+def test_one_expert_twice_and_for_all():
+    T, topk, E, H, I = 40, 4, 7, 160, 96
+    x, w, ids, weights = make(T, topk, E, H, I, 4)
+    ids[:] = 5
+    ids[3] = [2, 5, 2, 2]
+    want, bound = definition(x, w, ids, weights, torch.finfo(F32).eps)
+    y = torch.empty(T, H, device="cuda")
+    sq.sq_mx4_moe(*on_gpu(x, w, ids, weights), y)
+    check(y, want, bound)
+
+
+def test_a_token_with_nan_spoils_itself_alone():
+    T, topk, E, H, I = 6, 2, 4, 128, 128
+    x, w, ids, weights = make(T, topk, E, H, I, 5)
+    t = on_gpu(x, w, ids, weights)
+    y, z = torch.empty(T, H, device="cuda"), torch.empty(T, H, device="cuda")
+    sq.sq_mx4_moe(*t, y)
+    sx = x[1].copy()
+    sx[mx4.tile_index(T, H)[2, 1]] = 255
+    t[1] = torch.from_numpy(sx).cuda()
+    sq.sq_mx4_moe(*t, z)
+    assert torch.isnan(z[2]).all()
+    keep = [i for i in range(T) if i != 2]
+    assert torch.equal(y[keep], z[keep])

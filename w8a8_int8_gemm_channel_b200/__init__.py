@@ -25,6 +25,9 @@ The raw entry points keep the C names and take caller-allocated outputs:
     sq_mx4_dequant(q, sc, out)
     sq_mx4_gemm(xq, sx, wq, sw, y, workspace)
     sq_mx4_linear(x, s, wq, sw, y, workspace)
+    sq_mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, y, workspace)   a few tokens through their experts
+    sq_residual_norm_quant(b, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx)   norms around a block, int8 out
+    sq_residual_norm_quant_mx4(...)             the same, MXFP4 out
     sq_device_status()
 
 ``calibrate``, ``prepare_weight`` and ``linear`` are conveniences that allocate
@@ -73,6 +76,10 @@ ABI_SYMBOLS = (
     "sq_mx4_gemm",
     "sq_mx4_linear_workspace_size",
     "sq_mx4_linear",
+    "sq_mx4_moe_workspace_size",
+    "sq_mx4_moe",
+    "sq_residual_norm_quant",
+    "sq_residual_norm_quant_mx4",
     "sq_device_status",
     "sq_selftest_wait_timeout",
 )
@@ -121,6 +128,10 @@ def _declare(lib):
         "sq_mx4_gemm": ([P, P, P, P, I, I, I, P, E, P, Z, P], E),
         "sq_mx4_linear_workspace_size": ([I, I, I], Z),
         "sq_mx4_linear": ([P, E, P, P, P, I, I, I, P, E, P, Z, P], E),
+        "sq_mx4_moe_workspace_size": ([I, I, I, I, I], Z),
+        "sq_mx4_moe": ([P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P, E, P, Z, P], E),
+        "sq_residual_norm_quant": ([P, E, I, I, P, P, I, F, P, P, P, F, P, P, P], E),
+        "sq_residual_norm_quant_mx4": ([P, E, I, I, P, P, I, F, P, P, P, F, P, P, P], E),
         "sq_device_status": ([P, ctypes.POINTER(ctypes.c_uint32)], E),
         "sq_selftest_wait_timeout": ([ctypes.c_uint32, P], E),
     }
@@ -463,6 +474,65 @@ def sq_mx4_linear(x, s, wq, sw, y, workspace=None, stream=None):
                                                     *_ws_args(workspace), _stream(stream)))
 
 
+def sq_mx4_moe_workspace_size(T: int, topk: int, E: int, H: int, I: int) -> int:
+    return int(lib().sq_mx4_moe_workspace_size(T, topk, E, H, I))
+
+
+def sq_mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, y, workspace=None, stream=None):
+    """y [T, H] = the weighted sum over each token's experts ids [T, topk] (int32; outside [0, E): none) of the gated
+    layer wd[e] (silu(wg[e] x) * (wu[e] x)); x as codes xq [T, H / 2] and scale tiles sx."""
+    torch = _torch()
+    T, topk = ids.shape
+    E, I, H2 = wg.shape
+    H = H2 * 2
+    _need(ids.dtype is torch.int32 and weights.dtype is torch.float32 and tuple(weights.shape) == (T, topk),
+          "ids: int32, weights: float32, both [T, topk]")
+    _need(tuple(wu.shape) == (E, I, H2) and tuple(wd.shape) == (E, H, I // 2) and
+          wg.dtype is wu.dtype is wd.dtype is torch.uint8, "wg, wu: uint8 [E, I, H / 2], wd: uint8 [E, H, I / 2]")
+    up, down = -(-I // 128) * -(-H // 128) * 512, -(-H // 128) * -(-I // 128) * 512
+    _need(sg.dtype is su.dtype is sd.dtype is torch.uint8 and tuple(sg.shape) == tuple(su.shape) == (E, up) and
+          tuple(sd.shape) == (E, down), f"scales: uint8, sg and su {(E, up)}, sd {(E, down)}")
+    _need(tuple(y.shape) == (T, H), f"y: shape {(T, H)}")
+    _same_device(y, xq, sx, ids, weights, wg, sg, wu, su, wd, sd, workspace)
+    with _on_device_of(y):
+        if workspace is None:
+            workspace = torch.empty(sq_mx4_moe_workspace_size(T, topk, E, H, I), dtype=torch.uint8, device=y.device)
+        _check("sq_mx4_moe", lib().sq_mx4_moe(
+            *_mx4_ptrs(T, H, xq, sx), _ptr(ids), _ptr(weights), T, topk, E, H, I, _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su),
+            _ptr(wd), _ptr(sd), _ptr(y), _dtype_code(y), *_ws_args(workspace), _stream(stream)))
+
+
+def _residual_norm(name, b, gamma, gate, gate_tokens, c, r, r_out, g, eps, q, sx, stream):
+    torch = _torch()
+    M, K = b.shape
+    _need(tuple(r.shape) == tuple(r_out.shape) == (M, K) and b.dtype is r.dtype is r_out.dtype,
+          f"b, r and r_out: shape {(M, K)} and one dtype")
+    _need(gamma is None or (gamma.dtype is torch.float32 and gamma.numel() == K), f"gamma: float32 of {K} values")
+    _need(g.dtype is torch.float32 and g.numel() == K, f"g: float32 of {K} values")
+    if gate is not None:
+        _need(gate_tokens >= 1 and gate.dtype is b.dtype and gate.shape[-1] == K and
+              gate.numel() >= -(-M // gate_tokens) * K, "gate: b's dtype, a row for every gate_tokens tokens")
+    _same_device(b, gamma, gate, r, r_out, g, q, sx)
+    with _on_device_of(b):
+        _check(name, getattr(lib(), name)(_ptr(b), _dtype_code(b), M, K, _ptr(gamma), _ptr(gate), int(gate_tokens),
+                                          float(c), _ptr(r), _ptr(r_out), _ptr(g), float(eps), _ptr(q), _ptr(sx),
+                                          _stream(stream)))
+
+
+def sq_residual_norm_quant(b, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx, stream=None):
+    """r_out = r + c * gate * rmsnorm(b, gamma) (gamma, gate: None to leave out; r_out may be r); xq [M, K] int8 and
+    sx [M]: rmsnorm(r_out, g) quantised per token.  Token m uses gate row m // gate_tokens."""
+    _need(xq.dtype is _torch().int8 and tuple(xq.shape) == tuple(b.shape), f"xq: int8 of shape {tuple(b.shape)}")
+    _need(sx.dtype is _torch().float32 and sx.numel() == b.shape[0], f"sx: float32 of {b.shape[0]} values")
+    _residual_norm("sq_residual_norm_quant", b, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx, stream)
+
+
+def sq_residual_norm_quant_mx4(b, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx, stream=None):
+    """sq_residual_norm_quant with MXFP4 codes xq [M, K / 2] and scale tiles sx."""
+    _mx4_ptrs(*b.shape, xq, sx)
+    _residual_norm("sq_residual_norm_quant_mx4", b, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx, stream)
+
+
 def sq_device_status(stream=None) -> Tuple[int, int]:
     code = ctypes.c_uint32(0)
     st = lib().sq_device_status(_stream(stream), ctypes.byref(code))
@@ -539,4 +609,12 @@ def mx4_linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
     """y = mx4(x / s) w^T with a torch-allocated output."""
     y = _torch().empty(x.shape[0], wq.shape[0], dtype=out_dtype or x.dtype, device=x.device)
     sq_mx4_linear(x, s, wq, sw, y, workspace, stream)
+    return y
+
+
+def mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, out_dtype=None, workspace=None, stream=None):
+    """A few tokens through their experts with a torch-allocated output (bfloat16 unless out_dtype says otherwise)."""
+    torch = _torch()
+    y = torch.empty(ids.shape[0], wd.shape[1], dtype=out_dtype or torch.bfloat16, device=xq.device)
+    sq_mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, y, workspace, stream)
     return y

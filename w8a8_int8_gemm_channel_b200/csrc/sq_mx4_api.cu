@@ -13,7 +13,9 @@
 #include "sq_host.cuh"
 #include "sq_mx4.cuh"
 #include "sq_mx4_gemm.cuh"
+#include "sq_mx4_moe.cuh"
 #include "sq_mx4_stream.cuh"
+#include "sq_resnorm.cuh"
 
 namespace sq {
 
@@ -289,6 +291,156 @@ inline Mx4LinearWs mx4_linear_ws(int64_t M, int64_t N, int64_t K)
     return w;
 }
 
+// ---- experts layer for few tokens ------------------------------------------------
+// Workspace: h's codes and scale tiles (a tile per expert in use and 128
+// values), then the down projection's counters and partial tiles.
+struct Mx4MoeWs {
+    size_t hs = 0, cnt = 0, slots = 0, total = 0;
+    int64_t groups = 0;  // experts that can be in use at once
+    int ncnt = 0;
+};
+
+inline Mx4MoeWs mx4_moe_ws(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
+{
+    Mx4MoeWs w;
+    w.groups = std::min(E, T * topk);
+    w.hs = round256(static_cast<size_t>(w.groups * T) * static_cast<size_t>(I / 2));
+    w.cnt = w.hs + static_cast<size_t>(w.groups) * scale_bytes(1, I);
+    w.ncnt = static_cast<int>((H + 127) / 128);
+    w.slots = w.cnt + round256(static_cast<size_t>(w.ncnt) * sizeof(int));
+    w.total = w.slots + static_cast<size_t>(kMx4MaxCtas) * 2 * mx4_bnx(T) * 128 * sizeof(float);
+    return w;
+}
+
+sq_status check_mx4_moe_dims(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
+{
+    if (T < 1 || topk < 1 || E < 1 || !mx4_dims(1, H) || !mx4_dims(1, I))
+        return SQ_ERR_INVALID_ARG;
+    if (T > sq::kMx4MaxTokens || topk > sq::kMx4MaxSlots || T * topk > sq::kMx4MaxSlots || E > sq::kMx4MaxExperts ||
+        H > kMx4MaxDim || I > kMx4MaxDim || E * std::max(H, I) > (int64_t{1} << 30))
+        return SQ_ERR_UNSUPPORTED;
+    return SQ_OK;
+}
+
+struct Mx4MoeCall {
+    const uint8_t *xq, *sx, *wg, *sg, *wu, *su, *wd, *sd;
+    sq::Mx4MoeArgs route;
+    int64_t T, H, I;
+    void *y;
+    uint8_t *ws;
+    Mx4MoeWs L;
+};
+
+template <int BNX, int OUT>
+sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
+{
+    using Up = sq::Mx4UpCfg<BNX>;
+    using Cfg = sq::Mx4StreamCfg<BNX>;
+    DeviceInfo di;
+    if (!device_info(di))
+        return SQ_ERR_CUDA;
+    auto up = sq::mx4_moe_up_kernel<BNX>;
+    auto down = sq::mx4_stream_kernel<BNX, OUT, true>;
+    static std::atomic<uint64_t> up_done{0}, down_done{0};
+    if (!ensure_smem_attr(up, Up::SMEM_BYTES, up_done) || !ensure_smem_attr(down, kMaxDynSmem, down_done))
+        return SQ_ERR_CUDA;
+    uint8_t *hq = c.ws, *hs = c.ws + c.L.hs;
+    int *cnt = reinterpret_cast<int *>(c.ws + c.L.cnt);
+    float *slots = reinterpret_cast<float *>(c.ws + c.L.slots);
+    const int64_t E = c.route.E, RI = (c.I + 127) / 128, RH = (c.H + 127) / 128;
+    CUtensorMap tg, tsg, tu, tsu, tx, tsx, td, tsd, th, tsh;
+    if (!make_tmap_mx4(&tg, c.wg, E * c.I, c.H, 32) || !make_tmap_scales(&tsg, c.sg, E * RI, c.H, 1) ||
+        !make_tmap_mx4(&tu, c.wu, E * c.I, c.H, 32) || !make_tmap_scales(&tsu, c.su, E * RI, c.H, 1) ||
+        !make_tmap_mx4(&tx, c.xq, c.T, c.H, BNX) || !make_tmap_scales(&tsx, c.sx, 1, c.H, 1) ||
+        !make_tmap_mx4(&td, c.wd, E * c.H, c.I, 128) || !make_tmap_scales(&tsd, c.sd, E * RH, c.I, 1) ||
+        !make_tmap_mx4(&th, hq, c.L.groups * c.T, c.I, BNX) || !make_tmap_scales(&tsh, hs, c.L.groups, c.I, 1))
+        return SQ_ERR_CUDA;
+    const int ctas = static_cast<int>(std::min<int64_t>(di.sms, kMx4MaxCtas));
+    sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kDecThreads), Up::SMEM_BYTES, st, 0, 0,
+                                tg, tsg, tu, tsu, tx, tsx, hq, hs, cnt, c.L.ncnt, static_cast<int>(c.T),
+                                static_cast<int>(c.H), static_cast<int>(c.I), c.route);
+    if (r != SQ_OK)
+        return r;
+    constexpr int stages = BNX == 128 ? 6 : 8;
+    constexpr int smem = sq::mx4_stream_smem(Cfg::STAGE_BYTES, stages, true);
+    static_assert(smem <= kMaxDynSmem && stages <= Cfg::MAX_STAGES, "shared memory");
+    return launch_kernel(down, dim3(static_cast<unsigned>(ctas)), dim3(sq::kDecThreads), smem, st, 0, 0, td, tsd, th, tsh,
+                         c.y, slots, cnt, static_cast<int>(c.T), static_cast<int>(c.H), static_cast<int>(c.I), ctas,
+                         stages, 1, c.route);
+}
+
+template <int OUT>
+sq_status launch_mx4_moe_bnx(const Mx4MoeCall &c, cudaStream_t st)
+{
+    switch (mx4_bnx(c.T)) {
+    case 32: return launch_mx4_moe<32, OUT>(c, st);
+    case 64: return launch_mx4_moe<64, OUT>(c, st);
+    default: return launch_mx4_moe<128, OUT>(c, st);
+    }
+}
+
+// ---- norms around a block --------------------------------------------------------
+template <typename T, bool MX4, int CH, int THREADS, bool CACHE>
+sq_status launch_res_norm_cfg(const sq::ResArgs &p, int64_t sms, cudaStream_t st)
+{
+    auto kernel = sq::res_norm_kernel<T, MX4, CH, THREADS, CACHE>;
+    const int smem = CACHE ? static_cast<int>(2 * p.K * sizeof(float)) : 0;
+    static std::atomic<uint64_t> attr_done{0};
+    if (CACHE && !ensure_smem_attr(kernel, kMaxDynSmem - 1024, attr_done))
+        return SQ_ERR_CUDA;
+    int64_t blocks = p.M;
+    if (CACHE) {
+        // one wave: the CTAs an SM holds for this shared memory and 2048 threads
+        const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(2048 / THREADS, kSmSmemBytes / (smem + 2048)));
+        blocks = std::min(p.M, per_sm * sms);
+    }
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), smem, st, 0, 0, p);
+}
+
+template <typename T, bool MX4>
+sq_status launch_res_norm(const sq::ResArgs &p, cudaStream_t st)
+{
+    DeviceInfo di;
+    if (!device_info(di))
+        return SQ_ERR_CUDA;
+    const int64_t chunks = p.K / 8, sms = di.sms;
+    if (p.M < 4 * sms) {  // few rows: every SM has one or two CTAs, each row spread wide
+        if (chunks <= 512)
+            return launch_res_norm_cfg<T, MX4, 1, 512, false>(p, sms, st);
+        if (chunks <= 1024)
+            return launch_res_norm_cfg<T, MX4, 2, 512, false>(p, sms, st);
+    } else {
+        if (chunks <= 256)
+            return launch_res_norm_cfg<T, MX4, 1, 256, true>(p, sms, st);
+        if (chunks <= 512)
+            return launch_res_norm_cfg<T, MX4, 2, 256, true>(p, sms, st);
+        if (chunks <= 1024)
+            return launch_res_norm_cfg<T, MX4, 4, 256, true>(p, sms, st);
+    }
+    if constexpr (sizeof(T) == 2)
+        if (chunks > 2048)
+            return launch_res_norm_cfg<T, MX4, 8, 512, false>(p, sms, st);
+    return launch_res_norm_cfg<T, MX4, 4, 512, false>(p, sms, st);
+}
+
+// int64 the tokens that share a gate row; gate and gamma may be NULL
+sq_status residual_norm(const void *b, sq_dtype dt, int64_t M, int64_t K, const float *gamma, const void *gate,
+                        int64_t gate_tokens, float c, const void *r, void *r_out, const float *g, float eps, uint8_t *q,
+                        void *sx, bool mx4, sq_stream_t stream)
+{
+    if (!ok_ptr(b) || !valid_dtype(dt) || M < 1 || K < 16 || K % (mx4 ? 32 : 16) != 0 || !aligned16(gamma) ||
+        !aligned16(gate) || (gate != nullptr && gate_tokens < 1) || !std::isfinite(c) || !ok_ptr(r) || !ok_ptr(r_out) ||
+        b == r_out || !ok_ptr(g) || !(eps >= 0.0f) || !std::isfinite(eps) || !ok_ptr(q) || !ok_ptr(sx))
+        return SQ_ERR_INVALID_ARG;
+    if (K > (dt == SQ_BF16 ? 32768 : 16384) || M > kMx4MaxDim)
+        return SQ_ERR_UNSUPPORTED;
+    const sq::ResArgs p{b, r, gate, gamma, g, r_out, q, sx, M, K, gate == nullptr ? 1 : gate_tokens, c, eps};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dt == SQ_BF16)
+        return mx4 ? launch_res_norm<__nv_bfloat16, true>(p, st) : launch_res_norm<__nv_bfloat16, false>(p, st);
+    return mx4 ? launch_res_norm<float, true>(p, st) : launch_res_norm<float, false>(p, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -385,6 +537,46 @@ sq_status sq_mx4_linear(const void *x, sq_dtype in_dt, const float *s, const uin
         return r;
     return out_dt == SQ_BF16 ? launch_mx4_gemm<OUT_BF16>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st)
                              : launch_mx4_gemm<OUT_F32>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st);
+}
+
+size_t sq_mx4_moe_workspace_size(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
+{
+    return check_mx4_moe_dims(T, topk, E, H, I) == SQ_OK ? mx4_moe_ws(T, topk, E, H, I).total : 0;
+}
+
+sq_status sq_mx4_moe(const uint8_t *xq, const uint8_t *sx, const int32_t *ids, const float *weights, int64_t T,
+                     int64_t topk, int64_t E, int64_t H, int64_t I, const uint8_t *wg, const uint8_t *sg,
+                     const uint8_t *wu, const uint8_t *su, const uint8_t *wd, const uint8_t *sd, void *y,
+                     sq_dtype out_dt, void *workspace, size_t ws_bytes, sq_stream_t stream)
+{
+    if (!ok_ptr(xq) || !ok_ptr(sx) || !ok_ptr(ids) || !ok_ptr(weights) || !ok_ptr(wg) || !ok_ptr(sg) || !ok_ptr(wu) ||
+        !ok_ptr(su) || !ok_ptr(wd) || !ok_ptr(sd) || !ok_ptr(y) || !valid_dtype(out_dt))
+        return SQ_ERR_INVALID_ARG;
+    const sq_status r = check_mx4_moe_dims(T, topk, E, H, I);
+    if (r != SQ_OK)
+        return r;
+    const Mx4MoeWs L = mx4_moe_ws(T, topk, E, H, I);
+    if (!ok_ptr(workspace) || ws_bytes < L.total)
+        return SQ_ERR_INVALID_ARG;
+    const Mx4MoeCall c{xq, sx, wg, sg, wu, su, wd, sd, {ids, weights, static_cast<int>(topk), static_cast<int>(E)},
+                       T,  H,  I,  y,  static_cast<uint8_t *>(workspace), L};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return out_dt == SQ_BF16 ? launch_mx4_moe_bnx<OUT_BF16>(c, st) : launch_mx4_moe_bnx<OUT_F32>(c, st);
+}
+
+sq_status sq_residual_norm_quant(const void *b, sq_dtype dt, int64_t M, int64_t K, const float *gamma,
+                                 const void *gate, int64_t gate_tokens, float c, const void *r, void *r_out,
+                                 const float *g, float eps, int8_t *xq, float *sx, sq_stream_t stream)
+{
+    return residual_norm(b, dt, M, K, gamma, gate, gate_tokens, c, r, r_out, g, eps, reinterpret_cast<uint8_t *>(xq), sx,
+                         false, stream);
+}
+
+sq_status sq_residual_norm_quant_mx4(const void *b, sq_dtype dt, int64_t M, int64_t K, const float *gamma,
+                                     const void *gate, int64_t gate_tokens, float c, const void *r, void *r_out,
+                                     const float *g, float eps, uint8_t *xq, uint8_t *sx, sq_stream_t stream)
+{
+    return residual_norm(b, dt, M, K, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx, true, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,307 @@
+// sq_resnorm.cuh -- the norms on both sides of a residual addition, fused with
+// the gate, the residual scale and the next linear's quantiser.
+//
+//   n  = (b * rb) * gamma        rb = RN(1 / sqrt(mean(b^2) + eps))   (gamma given; else n = b)
+//   u  = n * gate                                                     (gate given; else u = n)
+//   r' = RN_dt(r + u * c)
+//   a  = (r' * ra) * g           ra = RN(1 / sqrt(mean(r'^2) + eps))
+//   then a's int8 codes with one scale a token, or its MXFP4 codes and scales
+//
+// every step one fp32 operation, rounded to nearest; the mean squares are sums
+// of exact squares in fp64, so codes do not hang on the order of a fp32 sum.
+//
+// Bound: memory.  A token is read once and r' written once: a CTA holds a row's
+// b and r in registers (CH chunks of 8 values a thread) from the load to the
+// codes, across the two or three block-wide reductions the definition needs.
+// The per-channel factors gamma and g, 8 bytes a value against the 6.6 a bf16
+// value moves, would make L2 the bound if every row fetched them; with several
+// rows a CTA they are staged in shared memory once, and the next row's loads are
+// in flight while the present row is reduced.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "sq_mx4.cuh"
+#include "sq_ptx.cuh"
+
+namespace sq {
+
+template <typename T>
+struct ResRaw;  // 8 values as loaded
+template <>
+struct ResRaw<__nv_bfloat16> {
+    uint4 a;
+};
+template <>
+struct ResRaw<float> {
+    float4 a, b;
+};
+
+__device__ __forceinline__ void res_load(ResRaw<__nv_bfloat16> &r, const __nv_bfloat16 *p)
+{
+    r.a = *reinterpret_cast<const uint4 *>(p);
+}
+__device__ __forceinline__ void res_load(ResRaw<float> &r, const float *p)
+{
+    r.a = reinterpret_cast<const float4 *>(p)[0];
+    r.b = reinterpret_cast<const float4 *>(p)[1];
+}
+__device__ __forceinline__ void res_zero(ResRaw<__nv_bfloat16> &r) { r.a = make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void res_zero(ResRaw<float> &r) { r.a = r.b = make_float4(0, 0, 0, 0); }
+__device__ __forceinline__ void res_values(const ResRaw<__nv_bfloat16> &r, float (&v)[8]) { bf16x8_to_f32(r.a, v); }
+__device__ __forceinline__ void res_values(const ResRaw<float> &r, float (&v)[8])
+{
+    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w, v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
+}
+// rounds to T and stores; `r` keeps what was stored
+__device__ __forceinline__ void res_store(ResRaw<__nv_bfloat16> &r, __nv_bfloat16 *p, const float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p) = r.a;
+}
+__device__ __forceinline__ void res_store(ResRaw<float> &r, float *p, const float (&v)[8])
+{
+    r.a = make_float4(v[0], v[1], v[2], v[3]);
+    r.b = make_float4(v[4], v[5], v[6], v[7]);
+    reinterpret_cast<float4 *>(p)[0] = r.a;
+    reinterpret_cast<float4 *>(p)[1] = r.b;
+}
+
+__device__ __forceinline__ double res_squares(const float (&v)[8])
+{
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        s = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), s);
+    return s;
+}
+
+// 1 / RMS from a row's sum of squares: every thread's `s` summed over the
+// block.  `buf` [32] doubles; `out` one float; buf and out are free again after
+// the caller's next barrier.
+template <int THREADS>
+__device__ __forceinline__ float res_rinv(double s, double inv_k, float eps, double *buf, volatile float *out)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
+        buf[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        double t = lane < THREADS / 32 ? buf[lane] : 0.0;
+#pragma unroll
+        for (int d = THREADS / 64; d > 0; d >>= 1)
+            t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+        const double ms = t * inv_k + static_cast<double>(eps);
+        if (lane == 0)
+            *out = ms > 0.0 ? static_cast<float>(rsqrt(ms)) : (ms == 0.0 ? 0.0f : static_cast<float>(ms));
+    }
+    __syncthreads();
+    return *out;
+}
+
+template <int THREADS>
+__device__ __forceinline__ float res_max(float m, float *buf)
+{
+    uint32_t u = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));  // m >= 0
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
+        buf[warp] = __uint_as_float(u);
+    __syncthreads();
+    u = __reduce_max_sync(0xFFFFFFFFu, lane < THREADS / 32 ? __float_as_uint(buf[lane]) : 0u);
+    return __uint_as_float(u);
+}
+
+// clamp(round_half_even(RN(a / sx)), -127, 127) of 8 values.  a * RN(1 / sx) is
+// within 127 * 2^-23 + 127 * 2^-24 < 2.5e-5 of RN(a / sx), so only a product
+// that near to a half-integer (or a scale too small for a normal reciprocal)
+// needs the division.
+__device__ __forceinline__ uint2 res_int8(const float (&a)[8], float sx, float inv, bool exact)
+{
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float t = __fmul_rn(a[i], inv);
+        const float q = rintf(t);
+        if (exact || fabsf(fabsf(t - q) - 0.5f) < 2.5e-5f)
+            t = sx > 0.0f ? __fdiv_rn(a[i], sx) : 0.0f;
+        const int c = max(-127, min(127, __float2int_rn(t)));
+        w[i >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (i & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+struct ResArgs {
+    const void *b, *r, *gate;
+    const float *gamma, *g;
+    void *r_out;
+    uint8_t *q;   // int8 [M, K] or MXFP4 codes [M, K / 2]
+    void *sx;     // float [M] or scale tiles
+    int64_t M, K, gate_tokens;
+    float c, eps;
+};
+
+// CH: chunks of 8 values a thread holds (K <= 8 * CH * THREADS); CACHE: gamma and
+// g in shared memory.
+template <typename T, bool MX4, int CH, int THREADS, bool CACHE>
+__global__ void __launch_bounds__(THREADS) res_norm_kernel(const ResArgs p)
+{
+    pdl_prologue();
+    extern __shared__ float factors[];  // [2][K] with CACHE
+    __shared__ double sum_b[32], sum_r[32];
+    __shared__ float rinv_b, rinv_r, top_s[32];
+    constexpr bool AHEAD = CACHE && CH * sizeof(T) <= 8;  // the next row's loads in flight (registers allow)
+    const int64_t K = p.K, KT = (K + 127) >> 7;
+    const double inv_k = 1.0 / static_cast<double>(K);
+    const T *b = static_cast<const T *>(p.b), *r = static_cast<const T *>(p.r), *gate = static_cast<const T *>(p.gate);
+    T *r_out = static_cast<T *>(p.r_out);
+    auto chunk = [&](int i) { return static_cast<int64_t>(i) * THREADS + threadIdx.x; };
+
+    if constexpr (CACHE) {
+        for (int64_t k = threadIdx.x * 4; k < K; k += THREADS * 4) {
+            if (p.gamma != nullptr)
+                *reinterpret_cast<float4 *>(factors + k) = __ldg(reinterpret_cast<const float4 *>(p.gamma + k));
+            *reinterpret_cast<float4 *>(factors + K + k) = __ldg(reinterpret_cast<const float4 *>(p.g + k));
+        }
+        __syncthreads();
+    }
+    auto factor = [&](const float *global, int64_t at, int64_t col, float (&f)[8]) {
+        if constexpr (CACHE) {
+            const float4 x = *reinterpret_cast<const float4 *>(factors + at + col);
+            const float4 y = *reinterpret_cast<const float4 *>(factors + at + col + 4);
+            f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+        } else {
+            load8<float>(global + col, f);
+        }
+    };
+    ResRaw<T> bv[CH], rv[CH], bn[AHEAD ? CH : 1], rn[AHEAD ? CH : 1];
+    auto fetch = [&](int64_t m, ResRaw<T> *x, ResRaw<T> *y) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int64_t col = chunk(i) * 8;
+            if (col < K && m < p.M) {
+                res_load(x[i], b + m * K + col);
+                res_load(y[i], r + m * K + col);
+            } else {
+                res_zero(x[i]);
+                res_zero(y[i]);
+            }
+        }
+    };
+    if constexpr (AHEAD)
+        fetch(blockIdx.x, bn, rn);
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                bv[i] = bn[i];
+                rv[i] = rn[i];
+            }
+            fetch(m + gridDim.x, bn, rn);
+        } else {
+            fetch(m, bv, rv);
+        }
+        float rb = 0.0f;
+        if (p.gamma != nullptr) {
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                float v[8];
+                res_values(bv[i], v);
+                s += res_squares(v);
+            }
+            rb = res_rinv<THREADS>(s, inv_k, p.eps, sum_b, &rinv_b);
+        }
+        const T *gr = gate == nullptr ? nullptr : gate + (m / p.gate_tokens) * K;
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int64_t col = chunk(i) * 8;
+            if (col >= K)
+                continue;
+            float u[8], f[8], o[8];
+            res_values(bv[i], u);
+            if (p.gamma != nullptr) {
+                factor(p.gamma, 0, col, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    u[j] = __fmul_rn(__fmul_rn(u[j], rb), f[j]);
+            }
+            if (gr != nullptr) {
+                load8<T>(gr + col, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    u[j] = __fmul_rn(u[j], f[j]);
+            }
+            res_values(rv[i], o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j] = __fadd_rn(o[j], __fmul_rn(u[j], p.c));
+            res_store(rv[i], r_out + m * K + col, o);
+            res_values(rv[i], o);
+            s += res_squares(o);
+        }
+        const float ra = res_rinv<THREADS>(s, inv_k, p.eps, sum_r, &rinv_r);
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int64_t c8 = chunk(i), col = c8 * 8;
+            const bool in_k = col < K;
+            float a[8], f[8];
+            res_values(rv[i], a);
+            if (in_k) {
+                factor(p.g, K, col, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    a[j] = __fmul_rn(__fmul_rn(a[j], ra), f[j]);
+            }
+            if constexpr (MX4) {
+                const int64_t kt = c8 >> 4;
+                if (__ballot_sync(0xFFFFFFFFu, kt < KT) != 0u)  // a whole warp behind the last scale tile has nothing to do
+                    mx4_store_chunk(a, in_k, reinterpret_cast<uint32_t *>(p.q + m * (K / 2) + c8 * 4),
+                                    (threadIdx.x & 15) == 0 && kt < KT
+                                        ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.sx) + mx4_scale_word(m, kt, KT))
+                                        : nullptr);
+            } else if (in_k) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = fmaxf(top, fabsf(a[j]));
+            }
+        }
+        if constexpr (!MX4) {
+            top = res_max<THREADS>(top, top_s);
+            const float sx = __fdiv_rn(top, 127.0f);
+            const bool exact = sx < 1e-30f;
+            const float inv = exact ? 0.0f : __frcp_rn(sx);
+            if (threadIdx.x == 0)
+                static_cast<float *>(p.sx)[m] = sx;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int64_t col = chunk(i) * 8;
+                if (col >= K)
+                    continue;
+                float a[8], f[8];
+                res_values(rv[i], a);
+                factor(p.g, K, col, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    a[j] = __fmul_rn(__fmul_rn(a[j], ra), f[j]);
+                *reinterpret_cast<uint2 *>(p.q + m * K + col) = res_int8(a, sx, inv, exact);
+            }
+        }
+    }
+    if constexpr (MX4)
+        mx4_zero_pad(static_cast<uint8_t *>(p.sx), p.M, KT, static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x,
+                     static_cast<int64_t>(gridDim.x) * THREADS);
+}
+
+}  // namespace sq
