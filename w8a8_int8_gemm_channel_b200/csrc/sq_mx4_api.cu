@@ -179,7 +179,7 @@ sq_status launch_mx4_stream(const uint8_t *xq, const uint8_t *sx, const uint8_t 
     if (debug_plan())
         std::fprintf(stderr, "sq mx4 stream M=%lld N=%lld K=%lld: BNX=%d ctas=%lld stages=%d\n", (long long)M,
                      (long long)N, (long long)K, BNX, (long long)G, stages);
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(G)), dim3(sq::kDecThreads), smem, st, 0, 0, tw, tsw, tx,
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(G)), dim3(sq::kMx4StreamThreads), smem, st, 0, 0, tw, tsw, tx,
                          tsx, y, slots, cnt, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
                          static_cast<int>(G), stages, 0, sq::Mx4MoeArgs{});
 }
@@ -356,7 +356,7 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
         !make_tmap_mx4(&th, hq, c.L.groups * c.T, c.I, BNX) || !make_tmap_scales(&tsh, hs, c.L.groups, c.I, 1))
         return SQ_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(di.sms, kMx4MaxCtas));
-    sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kDecThreads), Up::SMEM_BYTES, st, 0, 0,
+    sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), Up::SMEM_BYTES, st, 0, 0,
                                 tg, tsg, tu, tsu, tx, tsx, hq, hs, cnt, c.L.ncnt, static_cast<int>(c.T),
                                 static_cast<int>(c.H), static_cast<int>(c.I), c.route);
     if (r != SQ_OK)
@@ -364,7 +364,7 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
     constexpr int stages = BNX == 128 ? 6 : 8;
     constexpr int smem = sq::mx4_stream_smem(Cfg::STAGE_BYTES, stages, true);
     static_assert(smem <= kMaxDynSmem && stages <= Cfg::MAX_STAGES, "shared memory");
-    return launch_kernel(down, dim3(static_cast<unsigned>(ctas)), dim3(sq::kDecThreads), smem, st, 0, 0, td, tsd, th, tsh,
+    return launch_kernel(down, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), smem, st, 0, 0, td, tsd, th, tsh,
                          c.y, slots, cnt, static_cast<int>(c.T), static_cast<int>(c.H), static_cast<int>(c.I), ctas,
                          stages, 1, c.route);
 }
@@ -423,7 +423,7 @@ sq_status launch_res_norm(const sq::ResArgs &p, cudaStream_t st)
     return launch_res_norm_cfg<T, MX4, 4, 512, false>(p, sms, st);
 }
 
-// int64 the tokens that share a gate row; gate and gamma may be NULL
+// gate_tokens: tokens that share a gate row; gate and gamma may be NULL
 sq_status residual_norm(const void *b, sq_dtype dt, int64_t M, int64_t K, const float *gamma, const void *gate,
                         int64_t gate_tokens, float c, const void *r, void *r_out, const float *g, float eps, uint8_t *q,
                         void *sx, bool mx4, sq_stream_t stream)

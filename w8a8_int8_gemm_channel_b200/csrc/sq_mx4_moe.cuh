@@ -43,7 +43,7 @@ struct Mx4UpCfg {
     static constexpr int NACC = BNX == 128 ? 1 : 2;  // sets of (gate, up) accumulators
     static constexpr int SCALE_COLS = 24;
     static constexpr int TMEM_COLS = pow2_at_least(NACC * 2 * BNX + STAGES * SCALE_COLS, 32);
-    static constexpr int NUM_BARS = 2 * STAGES + 5;
+    static constexpr int NUM_BARS = 3 * STAGES + 5;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NUM_BARS * 8 + 24 + 2 * 16 +
                                       (kMx4MaxExperts / 32) * 4 + kMx4MaxExperts * 2;
     static_assert(TMEM_COLS <= 512 && SMEM_BYTES <= 232448, "limits");
@@ -63,7 +63,7 @@ __device__ __forceinline__ uint32_t mx4_code1(float v)
 }
 
 template <int BNX>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__(kMx4StreamThreads, 1)
     mx4_moe_up_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmSG,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmSU,
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     auto tfull_bar = [&](int b) { return bars + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](int b) { return bars + 8u * (2 * STAGES + 2 + b); };
     const uint32_t drain_bar = bars + 8u * (2 * STAGES + 4);
+    auto scale_bar = [&](int i) { return bars + 8u * (2 * STAGES + 5 + i); };
     const uint32_t misc_off = (bars - base) + 8u * Cfg::NUM_BARS;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gb + misc_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gb + misc_off + 4);
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(full_bar(i), 1);
             mbar_init(empty_bar(i), 1);
+            mbar_init(scale_bar(i), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
@@ -148,6 +150,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         return it;
     };
 
+    auto steps_of = [&](int kb) { return min(4, (H - kb * kMx4KB + 63) >> 6); };
     uint32_t issued_mask = 0, issued_parity = 0;
     bool mma_issued_any = false;
 
@@ -187,19 +190,56 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
         }
     } else if (warp == 1) {
+        const uint32_t leader = elect_one();
+        const uint32_t tS = tmem_base + Cfg::NACC * 2 * BNX;
+        const uint64_t g_desc = smem_desc_k_sw128(sG), u_desc = smem_desc_k_sw128(sU), x_desc = smem_desc_k_sw128(sX);
+        int stage = 0;
+        uint32_t phase = 0;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int64_t v = v0; v < v1 && ok;) {
+            v += item_at(v).nu;
+            if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
+                break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 2 * BNX);
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
+                    !bounded_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                tc_fence_after_sync();
+                const uint32_t t0 = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage);
+                const uint32_t w_at = static_cast<uint32_t>(stage * (Cfg::W_BYTES >> 4));
+                const uint64_t x = x_desc + static_cast<uint32_t>(stage * (Cfg::X_BYTES >> 4));
+                mx4_stage_mma<BNX>(leader, d, g_desc + w_at, x, t0, t0 + 16, steps_of(kb), kb == 0);
+                mx4_stage_mma<BNX>(leader, d + BNX, u_desc + w_at, x, t0 + 8, t0 + 16, steps_of(kb), kb == 0);
+                mma_issued_any = true;
+                mma_commit_warp(leader, empty_bar(stage));
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok)
+                break;
+            mma_commit_warp(leader, tfull_bar(acc));
+            if (++acc == Cfg::NACC) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    } else if (warp == 2) {
         if (lane == 0) {
             const uint32_t tS = tmem_base + Cfg::NACC * 2 * BNX;
-            int stage = 0;
-            uint32_t phase = 0;
-            int acc = 0;
-            uint32_t acc_phase = 0;
+            int stage = 0, last = -1;
+            uint32_t phase = 0, last_phase = 0;
             bool ok = true;
             for (int64_t v = v0; v < v1 && ok;) {
                 v += item_at(v).nu;
-                if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
-                    break;
-                tc_fence_after_sync();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 2 * BNX);
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag)) {
                         ok = false;
@@ -208,32 +248,26 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     tc_fence_after_sync();
                     const uint32_t t0 = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage);
                     const uint32_t s0 = sS + stage * 3 * Cfg::S_BYTES;
-                    const uint32_t x0 = sX + stage * Cfg::X_BYTES;
-                    const int steps = min(4, (H - kb * kMx4KB + 63) >> 6);
-                    mx4_stage_mma<BNX>(d, sG + stage * Cfg::W_BYTES, x0, s0, s0 + 2 * Cfg::S_BYTES, t0, t0 + 16, steps,
-                                       kb == 0, true);
-                    mx4_stage_mma<BNX>(d + BNX, sU + stage * Cfg::W_BYTES, x0, s0 + Cfg::S_BYTES, 0, t0 + 8, t0 + 16,
-                                       steps, kb == 0, false);
-                    mma_issued_any = true;
-                    mma_commit(empty_bar(stage));
+                    mx4_copy_scales(t0, s0, steps_of(kb));
+                    mx4_copy_scales(t0 + 8, s0 + Cfg::S_BYTES, steps_of(kb));
+                    mx4_copy_scales(t0 + 16, s0 + 2 * Cfg::S_BYTES, steps_of(kb));
+                    mma_commit(scale_bar(stage));
+                    last = stage;
+                    last_phase = phase;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (!ok)
-                    break;
-                mma_commit(tfull_bar(acc));
-                if (++acc == Cfg::NACC) {
-                    acc = 0;
-                    acc_phase ^= 1u;
-                }
             }
+            // the last copies have landed before the CTA may release TMEM
+            if (last >= 0)
+                bounded_wait(scale_bar(last), last_phase, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
         }
     } else {
-        // epilogue warps 2..5: warp w holds unit w % 4 of the tile, a channel a lane
+        // epilogue warps 3..6: warp w holds unit w % 4 of the tile, a channel a lane
         const int quarter = warp & 3;
-        const int et = threadIdx.x - 64;
+        const int et = threadIdx.x - 96;
         int acc = 0, wb = 0;
         uint32_t acc_phase = 0;
         for (int64_t v = v0; v < v1;) {
@@ -307,8 +341,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
 
     // ---- teardown ------------------------------------------------------------
-    if (warp == 1 && lane == 0 && *abort_flag && mma_issued_any) {
-        mma_commit(drain_bar);
+    if (warp == 1 && *abort_flag && mma_issued_any) {
+        __syncwarp();
+        mma_commit_warp(elect_one(), drain_bar);
         bounded_wait(drain_bar, 0, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
     }
     if (warp == 0 && lane == 0 && *abort_flag) {

@@ -22,10 +22,11 @@
 //
 // Scales.  A stage's scale tiles go from shared memory to TMEM columns that
 // belong to the stage (tcgen05.cp), so they are rewritten only after the
-// commit that freed the stage.
+// commit that freed the stage.  A warp of its own copies them, stages ahead of
+// the MMAs: issued by the MMA thread, the copies and the MMAs took turns.
 //
-// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM and MMA issue, warps
-// 2..5 epilogue.  Two accumulators, so a range's next tile (or expert)
+// Roles (224 threads): warp 0 TMA producer, warp 1 TMEM and MMA issue, warp 2
+// scale copies, warps 3..6 epilogue.  Two accumulators, so a range's next tile (or expert)
 // accumulates while the epilogue drains one.
 #pragma once
 
@@ -43,7 +44,7 @@ constexpr int kMx4KB = 256;          // values of K a stage holds (128 bytes of 
 constexpr int kMx4MaxTokens = 128;   // of the streaming kernels
 constexpr int kMx4MaxSlots = 1024;   // tokens x choices of the experts layer
 constexpr int kMx4MaxExperts = 1024;
-constexpr unsigned int kErrWaitMx4 = 0xC00;
+constexpr int kMx4StreamThreads = 224;
 
 template <int BNX>
 struct Mx4StreamCfg {
@@ -56,11 +57,11 @@ struct Mx4StreamCfg {
     static_assert(TMEM_COLS <= 512, "TMEM");
 };
 
-// ring, barriers (full, empty, tfull[2], tempty[2], drain), TMEM slot and two
+// ring, barriers (full, empty, tfull[2], tempty[2], drain, scales), TMEM slot and two
 // flags, routing weights of a group [128] and its mask [4], expert mask and list
 __host__ __device__ constexpr int mx4_stream_smem(int stage_bytes, int stages, bool moe)
 {
-    return 1024 + stages * stage_bytes + (2 * stages + 5) * 8 + 24 +
+    return 1024 + stages * stage_bytes + (3 * stages + 5) * 8 + 24 +
            (moe ? 2 * 512 + 2 * 16 + (kMx4MaxExperts / 32) * 4 + kMx4MaxExperts * 2 : 0);
 }
 
@@ -101,27 +102,26 @@ __device__ __forceinline__ int mx4_active_experts(const int *__restrict__ ids, i
     return *count;
 }
 
-// MMAs of one stage: the scale tiles into the stage's TMEM columns, then one
-// instruction per 64 values of K.  `atoms` scale tiles (128 values each) and
-// `steps` instructions are inside K.
-template <int N>
-__device__ __forceinline__ void mx4_stage_mma(uint32_t d, uint32_t a0, uint32_t b0, uint32_t sa, uint32_t sb,
-                                              uint32_t ta, uint32_t tb, int steps, bool first, bool copy_b)
+// The scale tiles of one operand's stage into its 8 TMEM columns; `steps` MMAs
+// of 64 values are inside K, two a tile.
+__device__ __forceinline__ void mx4_copy_scales(uint32_t taddr, uint32_t saddr, int steps)
 {
-    tmem_cp_scales(ta, smem_desc_scales(sa));
-    if (copy_b)
-        tmem_cp_scales(tb, smem_desc_scales(sb));
-    if (steps > 2) {
-        tmem_cp_scales(ta + 4, smem_desc_scales(sa + kMx4TileBytes));
-        if (copy_b)
-            tmem_cp_scales(tb + 4, smem_desc_scales(sb + kMx4TileBytes));
-    }
+    tmem_cp_scales(taddr, smem_desc_scales(saddr));
+    if (steps > 2)
+        tmem_cp_scales(taddr + 4, smem_desc_scales(saddr + kMx4TileBytes));
+}
+
+// The MMAs of one stage (a whole warp calls; a, b: descriptors of the stage's
+// operands, ta, tb: their scales in TMEM).
+template <int N>
+__device__ __forceinline__ void mx4_stage_mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t ta,
+                                              uint32_t tb, int steps, bool first)
+{
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (k < steps)
-            mma_mx4(d, smem_desc_k_sw128(a0 + 32 * k), smem_desc_k_sw128(b0 + 32 * k),
-                    (k & 1) ? idesc_mx4(128, N, 2) : idesc_mx4(128, N, 0), ta + 4 * (k >> 1), tb + 4 * (k >> 1),
-                    (first && k == 0) ? 0u : 1u);
+            mma_mx4_warp(leader, d, a + 2 * k, b + 2 * k, (k & 1) ? idesc_mx4(128, N, 2) : idesc_mx4(128, N, 0),
+                         ta + 4 * (k >> 1), tb + 4 * (k >> 1), (first && k == 0) ? 0u : 1u);
 }
 
 // The weight side of a launch.  Linear: G = 1, one matrix.  Experts: the group
@@ -133,7 +133,7 @@ struct Mx4MoeArgs {
 };
 
 template <int BNX, int OUT, bool MOE>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__(kMx4StreamThreads, 1)
     mx4_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW,
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
                       void *__restrict__ y, float *__restrict__ ws, int *__restrict__ cnt, int M, int N, int K,
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     auto tfull_bar = [&](int b) { return bars + 8u * (2 * stages + b); };
     auto tempty_bar = [&](int b) { return bars + 8u * (2 * stages + 2 + b); };
     const uint32_t drain_bar = bars + 8u * (2 * stages + 4);
-    const uint32_t misc_off = (bars - base) + 8u * (2 * stages + 5);
+    auto scale_bar = [&](int i) { return bars + 8u * (2 * stages + 5 + i); };
+    const uint32_t misc_off = (bars - base) + 8u * (3 * stages + 5);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gb + misc_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gb + misc_off + 4);
     volatile int *last_flag = reinterpret_cast<volatile int *>(gb + misc_off + 8);
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int i = 0; i < stages; ++i) {
             mbar_init(full_bar(i), 1);
             mbar_init(empty_bar(i), 1);
+            mbar_init(scale_bar(i), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
@@ -267,52 +269,79 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
         }
     } else if (warp == 1) {
+        const uint32_t leader = elect_one();
+        const uint32_t tS = tmem_base + 2 * BNX;  // scales: 16 columns a stage
+        const uint64_t w_desc = smem_desc_k_sw128(sW), x_desc = smem_desc_k_sw128(sX);
+        int stage = 0;
+        uint32_t phase = 0;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int64_t u = u0; u < u1 && ok;) {
+            // one accumulator: the k blocks of one tile and expert
+            const int kb0 = static_cast<int>(u % KB);
+            const int kb1 = static_cast<int>(min(static_cast<int64_t>(KB), kb0 + (u1 - u)));
+            u += kb1 - kb0;
+            if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
+                break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BNX);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
+                    !bounded_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                tc_fence_after_sync();
+                const uint32_t t0 = tS + 16u * stage;
+                mx4_stage_mma<BNX>(leader, d, w_desc + static_cast<uint32_t>(stage * (Cfg::W_BYTES >> 4)),
+                                   x_desc + static_cast<uint32_t>(stage * (Cfg::X_BYTES >> 4)), t0, t0 + 8, steps_of(kb),
+                                   kb == kb0);
+                mma_issued_any = true;
+                mma_commit_warp(leader, empty_bar(stage));
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok)
+                break;
+            mma_commit_warp(leader, tfull_bar(acc));
+            acc ^= 1;
+            if (acc == 0)
+                acc_phase ^= 1u;
+        }
+    } else if (warp == 2) {
         if (lane == 0) {
-            const uint32_t tS = tmem_base + 2 * BNX;  // scales: 16 columns a stage
-            int stage = 0;
-            uint32_t phase = 0;
-            int acc = 0;
-            uint32_t acc_phase = 0;
-            bool ok = true;
-            for (int64_t u = u0; u < u1 && ok;) {
-                // one accumulator: the k blocks of one tile and expert
-                const int kb0 = static_cast<int>(u % KB);
-                const int kb1 = static_cast<int>(min(static_cast<int64_t>(KB), kb0 + (u1 - u)));
-                u += kb1 - kb0;
-                if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
+            const uint32_t tS = tmem_base + 2 * BNX;
+            int stage = 0, last = -1;
+            uint32_t phase = 0, last_phase = 0;
+            for (int64_t u = u0; u < u1; ++u) {
+                if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag))
                     break;
                 tc_fence_after_sync();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BNX);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t t0 = tS + 16u * stage;
-                    mx4_stage_mma<BNX>(d, sW + stage * Cfg::W_BYTES, sX + stage * Cfg::X_BYTES,
-                                       sSW + stage * Cfg::S_BYTES, sSX + stage * Cfg::S_BYTES, t0, t0 + 8, steps_of(kb),
-                                       kb == kb0, true);
-                    mma_issued_any = true;
-                    mma_commit(empty_bar(stage));
-                    if (++stage == stages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                const uint32_t t0 = tS + 16u * stage;
+                const int steps = steps_of(static_cast<int>(u % KB));
+                mx4_copy_scales(t0, sSW + stage * Cfg::S_BYTES, steps);
+                mx4_copy_scales(t0 + 8, sSX + stage * Cfg::S_BYTES, steps);
+                mma_commit(scale_bar(stage));
+                last = stage;
+                last_phase = phase;
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
-                if (!ok)
-                    break;
-                mma_commit(tfull_bar(acc));
-                acc ^= 1;
-                if (acc == 0)
-                    acc_phase ^= 1u;
             }
+            // the last copies have landed before the CTA may release TMEM
+            if (last >= 0)
+                bounded_wait(scale_bar(last), last_phase, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
         }
     } else {
-        // epilogue warps 2..5: warp w reads TMEM lanes 32 (w % 4) .. +31
+        // epilogue warps 3..6: warp w reads TMEM lanes 32 (w % 4) .. +31
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;  // weight row within the tile
-        const int et = threadIdx.x - 64;      // 0..127
+        const int et = threadIdx.x - 96;      // 0..127
         int acc = 0, wb = 0;
         uint32_t acc_phase = 0;
         auto store = [&](const float (&o)[BNX], int64_t n) {
@@ -455,8 +484,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
 
     // ---- teardown ------------------------------------------------------------
-    if (warp == 1 && lane == 0 && *abort_flag && mma_issued_any) {
-        mma_commit(drain_bar);
+    if (warp == 1 && *abort_flag && mma_issued_any) {
+        __syncwarp();
+        mma_commit_warp(elect_one(), drain_bar);
         bounded_wait(drain_bar, 0, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
     }
     if (warp == 0 && lane == 0 && *abort_flag) {
