@@ -194,6 +194,10 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream=None) -> int:
     torch = _torch()
     if stream is None:
+        # the raw handle, where torch gives it: a Stream object costs more than a launch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -365,49 +369,44 @@ def _need(ok: bool, what: str):
 
 def _mx4_ptrs(rows: int, K: int, q, sc):
     """Device pointers of codes and scales, their sizes checked against [rows, K]."""
-    torch = _torch()
-    _need(q.dtype is torch.uint8 and tuple(q.shape) == (rows, K // 2), f"codes: uint8 of shape {(rows, K // 2)}")
-    _need(sc.dtype is torch.uint8 and sc.numel() >= -(-rows // 128) * -(-K // 128) * 512,
-          f"scales: uint8 of sq_mx4_scale_size({rows}, {K}) bytes")
-    return _ptr(q), _ptr(sc)
+    u8 = _torch().uint8
+    if q.dtype is not u8 or q.shape != (rows, K // 2):
+        raise ValueError(f"codes: uint8 of shape {(rows, K // 2)}")
+    if sc.dtype is not u8 or sc.numel() < -(-rows // 128) * -(-K // 128) * 512:
+        raise ValueError(f"scales: uint8 of sq_mx4_scale_size({rows}, {K}) bytes")
+    return q.data_ptr(), sc.data_ptr()
 
 
 def _mx4_factors(s, K: int):
     if s is None:
         return None
-    _need(s.dtype is _torch().float32 and s.numel() == K, f"s: float32 of {K} values")
-    return _ptr(s)
+    if s.dtype is not _torch().float32 or s.numel() != K:
+        raise ValueError(f"s: float32 of {K} values")
+    return s.data_ptr()
 
 
 def _ws_args(ws):
-    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
-class _on_device_of:
-    """Makes the device of `t` the current one for a call (its current stream is the default)."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, t):
-        torch = _torch()
-        self.guard = None
-        if t.is_cuda and t.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _same_device(first, *others):
-    d = first.device
-    for t in others:
-        if t is not None and t.device != d:
-            raise ValueError(f"tensors on {d} and {t.device}")
+def _call(name, stream, tensors, make_args):
+    """Calls an entry point with the tensors' device current: every tensor on one device and contiguous (None: left
+    out).  make_args() gives the arguments before the stream."""
+    torch = _torch()
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != d or d < 0 or not t.is_contiguous()):
+            if not t.is_cuda:
+                raise ValueError("libsq takes device tensors")
+            raise ValueError("libsq takes contiguous tensors" if t.get_device() == d else f"tensors on devices {d} and {t.get_device()}")
+    f = getattr(_lib or lib(), name)
+    if d == torch.cuda.current_device():
+        st = f(*make_args(), _stream(stream))
+    else:
+        with torch.cuda.device(d):
+            st = f(*make_args(), _stream(stream))
+    if st != SQ_OK:
+        raise SQError(name, st, status_string(st))
 
 
 def sq_mx4_scale_size(rows: int, K: int) -> int:
@@ -417,27 +416,21 @@ def sq_mx4_scale_size(rows: int, K: int) -> int:
 
 def sq_mx4_quant_act(x, s, xq, sx, stream=None):
     M, K = x.shape
-    _same_device(x, s, xq, sx)
-    with _on_device_of(x):
-        _check("sq_mx4_quant_act", lib().sq_mx4_quant_act(_ptr(x), _dtype_code(x), M, K, _mx4_factors(s, K),
-                                                          *_mx4_ptrs(M, K, xq, sx), _stream(stream)))
+    _call("sq_mx4_quant_act", stream, (x, s, xq, sx),
+          lambda: (x.data_ptr(), _dtype_code(x), M, K, _mx4_factors(s, K), *_mx4_ptrs(M, K, xq, sx)))
 
 
 def sq_mx4_quant_weight(w, s, wq, sw, stream=None):
     N, K = w.shape
-    _same_device(w, s, wq, sw)
-    with _on_device_of(w):
-        _check("sq_mx4_quant_weight", lib().sq_mx4_quant_weight(_ptr(w), _dtype_code(w), N, K, _mx4_factors(s, K),
-                                                                *_mx4_ptrs(N, K, wq, sw), _stream(stream)))
+    _call("sq_mx4_quant_weight", stream, (w, s, wq, sw),
+          lambda: (w.data_ptr(), _dtype_code(w), N, K, _mx4_factors(s, K), *_mx4_ptrs(N, K, wq, sw)))
 
 
 def sq_mx4_dequant(q, sc, out, stream=None):
     """out [rows, K] (float32 or bfloat16): the values the codes stand for."""
     rows, K = out.shape
-    _same_device(out, q, sc)
-    with _on_device_of(out):
-        _check("sq_mx4_dequant", lib().sq_mx4_dequant(*_mx4_ptrs(rows, K, q, sc), rows, K, _ptr(out), _dtype_code(out),
-                                                      _stream(stream)))
+    _call("sq_mx4_dequant", stream, (out, q, sc),
+          lambda: (*_mx4_ptrs(rows, K, q, sc), rows, K, out.data_ptr(), _dtype_code(out)))
 
 
 def sq_mx4_gemm_workspace_size(M: int, N: int, K: int) -> int:
@@ -448,12 +441,11 @@ def sq_mx4_gemm(xq, sx, wq, sw, y, workspace=None, stream=None):
     """y [M, N] = x w^T of the values the codes stand for (a workspace is allocated when none is given)."""
     M, N = y.shape
     K = xq.shape[1] * 2
-    _same_device(y, xq, sx, wq, sw, workspace)
-    with _on_device_of(y):
-        if workspace is None:
-            workspace = _torch().empty(sq_mx4_gemm_workspace_size(M, N, K), dtype=_torch().uint8, device=y.device)
-        _check("sq_mx4_gemm", lib().sq_mx4_gemm(*_mx4_ptrs(M, K, xq, sx), *_mx4_ptrs(N, K, wq, sw), M, N, K, _ptr(y),
-                                                _dtype_code(y), *_ws_args(workspace), _stream(stream)))
+    if workspace is None:
+        workspace = _torch().empty(sq_mx4_gemm_workspace_size(M, N, K), dtype=_torch().uint8, device=y.device)
+    _call("sq_mx4_gemm", stream, (y, xq, sx, wq, sw, workspace),
+          lambda: (*_mx4_ptrs(M, K, xq, sx), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(), _dtype_code(y),
+                   *_ws_args(workspace)))
 
 
 def sq_mx4_linear_workspace_size(M: int, N: int, K: int) -> int:
@@ -464,14 +456,13 @@ def sq_mx4_linear(x, s, wq, sw, y, workspace=None, stream=None):
     """y [M, N] = mx4(x / s) w^T (a workspace is allocated when none is given)."""
     M, K = x.shape
     N = wq.shape[0]
-    _same_device(x, s, wq, sw, y, workspace)
-    _need(tuple(y.shape) == (M, N), f"y: shape {(M, N)}")
-    with _on_device_of(x):
-        if workspace is None:
-            workspace = _torch().empty(sq_mx4_linear_workspace_size(M, N, K), dtype=_torch().uint8, device=x.device)
-        _check("sq_mx4_linear", lib().sq_mx4_linear(_ptr(x), _dtype_code(x), _mx4_factors(s, K),
-                                                    *_mx4_ptrs(N, K, wq, sw), M, N, K, _ptr(y), _dtype_code(y),
-                                                    *_ws_args(workspace), _stream(stream)))
+    if y.shape != (M, N):
+        raise ValueError(f"y: shape {(M, N)}")
+    if workspace is None:
+        workspace = _torch().empty(sq_mx4_linear_workspace_size(M, N, K), dtype=_torch().uint8, device=x.device)
+    _call("sq_mx4_linear", stream, (x, s, wq, sw, y, workspace),
+          lambda: (x.data_ptr(), _dtype_code(x), _mx4_factors(s, K), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(),
+                   _dtype_code(y), *_ws_args(workspace)))
 
 
 def sq_mx4_moe_workspace_size(T: int, topk: int, E: int, H: int, I: int) -> int:
@@ -484,45 +475,42 @@ def sq_mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, y, workspace=None, 
     torch = _torch()
     T, topk = ids.shape
     E, I, H2 = wg.shape
-    H = H2 * 2
-    _need(ids.dtype is torch.int32 and weights.dtype is torch.float32 and tuple(weights.shape) == (T, topk),
-          "ids: int32, weights: float32, both [T, topk]")
-    _need(tuple(wu.shape) == (E, I, H2) and tuple(wd.shape) == (E, H, I // 2) and
-          wg.dtype is wu.dtype is wd.dtype is torch.uint8, "wg, wu: uint8 [E, I, H / 2], wd: uint8 [E, H, I / 2]")
-    up, down = -(-I // 128) * -(-H // 128) * 512, -(-H // 128) * -(-I // 128) * 512
-    _need(sg.dtype is su.dtype is sd.dtype is torch.uint8 and tuple(sg.shape) == tuple(su.shape) == (E, up) and
-          tuple(sd.shape) == (E, down), f"scales: uint8, sg and su {(E, up)}, sd {(E, down)}")
-    _need(tuple(y.shape) == (T, H), f"y: shape {(T, H)}")
-    _same_device(y, xq, sx, ids, weights, wg, sg, wu, su, wd, sd, workspace)
-    with _on_device_of(y):
-        if workspace is None:
-            workspace = torch.empty(sq_mx4_moe_workspace_size(T, topk, E, H, I), dtype=torch.uint8, device=y.device)
-        _check("sq_mx4_moe", lib().sq_mx4_moe(
-            *_mx4_ptrs(T, H, xq, sx), _ptr(ids), _ptr(weights), T, topk, E, H, I, _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su),
-            _ptr(wd), _ptr(sd), _ptr(y), _dtype_code(y), *_ws_args(workspace), _stream(stream)))
+    H, u8 = H2 * 2, torch.uint8
+    if ids.dtype is not torch.int32 or weights.dtype is not torch.float32 or weights.shape != (T, topk):
+        raise ValueError("ids: int32, weights: float32, both [T, topk]")
+    if wu.shape != (E, I, H2) or wd.shape != (E, H, I // 2) or not (wg.dtype is wu.dtype is wd.dtype is u8):
+        raise ValueError("wg, wu: uint8 [E, I, H / 2], wd: uint8 [E, H, I / 2]")
+    kt_h, kt_i = -(-H // 128), -(-I // 128)
+    size = (E, kt_i * kt_h * 512)
+    if sg.shape != size or su.shape != size or sd.shape != size or not (sg.dtype is su.dtype is sd.dtype is u8):
+        raise ValueError(f"scales: uint8 {size}")
+    if y.shape != (T, H):
+        raise ValueError(f"y: shape {(T, H)}")
+    if workspace is None:
+        workspace = torch.empty(sq_mx4_moe_workspace_size(T, topk, E, H, I), dtype=u8, device=y.device)
+    _call("sq_mx4_moe", stream, (y, xq, sx, ids, weights, wg, sg, wu, su, wd, sd, workspace),
+          lambda: (*_mx4_ptrs(T, H, xq, sx), ids.data_ptr(), weights.data_ptr(), T, topk, E, H, I, wg.data_ptr(),
+                   sg.data_ptr(), wu.data_ptr(), su.data_ptr(), wd.data_ptr(), sd.data_ptr(), y.data_ptr(),
+                   _dtype_code(y), *_ws_args(workspace)))
 
 
 def _residual_norm(name, b, gamma, gate, gate_tokens, c, r, r_out, g, eps, q, sx, stream):
-    torch = _torch()
     M, K = b.shape
-    _need(tuple(r.shape) == tuple(r_out.shape) == (M, K) and b.dtype is r.dtype is r_out.dtype,
-          f"b, r and r_out: shape {(M, K)} and one dtype")
-    _need(gamma is None or (gamma.dtype is torch.float32 and gamma.numel() == K), f"gamma: float32 of {K} values")
-    _need(g.dtype is torch.float32 and g.numel() == K, f"g: float32 of {K} values")
-    if gate is not None:
-        _need(gate_tokens >= 1 and gate.dtype is b.dtype and gate.shape[-1] == K and
-              gate.numel() >= -(-M // gate_tokens) * K, "gate: b's dtype, a row for every gate_tokens tokens")
-    _same_device(b, gamma, gate, r, r_out, g, q, sx)
-    with _on_device_of(b):
-        _check(name, getattr(lib(), name)(_ptr(b), _dtype_code(b), M, K, _ptr(gamma), _ptr(gate), int(gate_tokens),
-                                          float(c), _ptr(r), _ptr(r_out), _ptr(g), float(eps), _ptr(q), _ptr(sx),
-                                          _stream(stream)))
+    if r.shape != b.shape or r_out.shape != b.shape or not (b.dtype is r.dtype is r_out.dtype):
+        raise ValueError(f"b, r and r_out: shape {(M, K)} and one dtype")
+    if gate is not None and (gate_tokens < 1 or gate.dtype is not b.dtype or gate.shape[-1] != K or
+                             gate.numel() < -(-M // gate_tokens) * K):
+        raise ValueError("gate: b's dtype, a row for every gate_tokens tokens")
+    _call(name, stream, (b, gamma, gate, r, r_out, g, q, sx),
+          lambda: (b.data_ptr(), _dtype_code(b), M, K, _mx4_factors(gamma, K), None if gate is None else gate.data_ptr(),
+                   int(gate_tokens), float(c), r.data_ptr(), r_out.data_ptr(), _mx4_factors(g, K), float(eps),
+                   q.data_ptr(), sx.data_ptr()))
 
 
 def sq_residual_norm_quant(b, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx, stream=None):
     """r_out = r + c * gate * rmsnorm(b, gamma) (gamma, gate: None to leave out; r_out may be r); xq [M, K] int8 and
     sx [M]: rmsnorm(r_out, g) quantised per token.  Token m uses gate row m // gate_tokens."""
-    _need(xq.dtype is _torch().int8 and tuple(xq.shape) == tuple(b.shape), f"xq: int8 of shape {tuple(b.shape)}")
+    _need(xq.dtype is _torch().int8 and xq.shape == b.shape, f"xq: int8 of shape {tuple(b.shape)}")
     _need(sx.dtype is _torch().float32 and sx.numel() == b.shape[0], f"sx: float32 of {b.shape[0]} values")
     _residual_norm("sq_residual_norm_quant", b, gamma, gate, gate_tokens, c, r, r_out, g, eps, xq, sx, stream)
 

@@ -63,9 +63,34 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, flo
     bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p)), v);
 }
 
-// Eight values scaled by `inv` as E2M1 codes, value i in bits 4i..4i+3.
-__device__ __forceinline__ uint32_t mx4_codes8(const float (&v)[8], float inv)
+// v[i] * f[i] and v[i] * f, two at a time (packed fp32, rounded like the scalar)
+__device__ __forceinline__ void mul8(float (&v)[8], const float (&f)[8])
 {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 t = f2_mul(make_float2(v[i], v[i + 1]), make_float2(f[i], f[i + 1]));
+        v[i] = t.x;
+        v[i + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void mul8(float (&v)[8], float f)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 t = f2_mul(make_float2(v[i], v[i + 1]), make_float2(f, f));
+        v[i] = t.x;
+        v[i + 1] = t.y;
+    }
+}
+
+// Eight values scaled by `inv` as E2M1 codes, value i in bits 4i..4i+3.
+__device__ __forceinline__ uint32_t mx4_codes8(const float (&x)[8], float inv)
+{
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = x[i];
+    mul8(v, inv);
     uint32_t d;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -74,8 +99,7 @@ __device__ __forceinline__ uint32_t mx4_codes8(const float (&v)[8], float inv)
         "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
         "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(d)
-        : "f"(v[0] * inv), "f"(v[1] * inv), "f"(v[2] * inv), "f"(v[3] * inv), "f"(v[4] * inv), "f"(v[5] * inv),
-          "f"(v[6] * inv), "f"(v[7] * inv));
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return d;
 }
 
@@ -183,11 +207,8 @@ __global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restr
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = rb + ty + static_cast<int64_t>(u) * TY;
-            if constexpr (OP != MX4_PLAIN) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[u][i] = __fmul_rn(v[u][i], f[i]);
-            }
+            if constexpr (OP != MX4_PLAIN)
+                mul8(v[u], f);
             const bool live = r < r1;
             mx4_store_chunk(v[u], in_k && live, reinterpret_cast<uint32_t *>(codes + r * (K / 2) + c * 4),
                             word_lane && live ? reinterpret_cast<uint32_t *>(scales + mx4_scale_word(r, kt, KT))

@@ -380,23 +380,21 @@ sq_status launch_mx4_moe_bnx(const Mx4MoeCall &c, cudaStream_t st)
 }
 
 // ---- norms around a block --------------------------------------------------------
-template <typename T, bool MX4, int CH, int THREADS, bool CACHE>
+template <typename T, bool MX4, int CH, int THREADS, bool CACHE, int BLOCKS>
 sq_status launch_res_norm_cfg(const sq::ResArgs &p, int64_t sms, cudaStream_t st)
 {
-    auto kernel = sq::res_norm_kernel<T, MX4, CH, THREADS, CACHE>;
+    auto kernel = sq::res_norm_kernel<T, MX4, CH, THREADS, CACHE, BLOCKS>;
     const int smem = CACHE ? static_cast<int>(2 * p.K * sizeof(float)) : 0;
     static std::atomic<uint64_t> attr_done{0};
-    if (CACHE && !ensure_smem_attr(kernel, kMaxDynSmem - 1024, attr_done))
+    if (CACHE && !ensure_smem_attr(kernel, kMaxDynSmem - 2048, attr_done))
         return SQ_ERR_CUDA;
-    int64_t blocks = p.M;
-    if (CACHE) {
-        // one wave: the CTAs an SM holds for this shared memory and 2048 threads
-        const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(2048 / THREADS, kSmSmemBytes / (smem + 2048)));
-        blocks = std::min(p.M, per_sm * sms);
-    }
+    const int64_t blocks = CACHE ? std::min<int64_t>(p.M, BLOCKS * sms) : p.M;  // with CACHE one wave
     return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), smem, st, 0, 0, p);
 }
 
+// Few rows: every row spread over 512 threads.  Enough rows for several a CTA:
+// the factors staged in shared memory, as many warps on an SM as the registers
+// of a row's chunks allow.
 template <typename T, bool MX4>
 sq_status launch_res_norm(const sq::ResArgs &p, cudaStream_t st)
 {
@@ -404,23 +402,24 @@ sq_status launch_res_norm(const sq::ResArgs &p, cudaStream_t st)
     if (!device_info(di))
         return SQ_ERR_CUDA;
     const int64_t chunks = p.K / 8, sms = di.sms;
-    if (p.M < 4 * sms) {  // few rows: every SM has one or two CTAs, each row spread wide
+    constexpr bool W = sizeof(T) == 2;
+    if (p.M < 4 * sms) {
         if (chunks <= 512)
-            return launch_res_norm_cfg<T, MX4, 1, 512, false>(p, sms, st);
+            return launch_res_norm_cfg<T, MX4, 1, 512, false, 2>(p, sms, st);
         if (chunks <= 1024)
-            return launch_res_norm_cfg<T, MX4, 2, 512, false>(p, sms, st);
+            return launch_res_norm_cfg<T, MX4, 2, 512, false, 2>(p, sms, st);
     } else {
         if (chunks <= 256)
-            return launch_res_norm_cfg<T, MX4, 1, 256, true>(p, sms, st);
+            return launch_res_norm_cfg<T, MX4, 1, 256, true, 4>(p, sms, st);
         if (chunks <= 512)
-            return launch_res_norm_cfg<T, MX4, 2, 256, true>(p, sms, st);
+            return launch_res_norm_cfg<T, MX4, 2, 256, true, W ? 4 : 2>(p, sms, st);
         if (chunks <= 1024)
-            return launch_res_norm_cfg<T, MX4, 4, 256, true>(p, sms, st);
+            return launch_res_norm_cfg<T, MX4, 4, 256, true, W ? 3 : 2>(p, sms, st);
     }
-    if constexpr (sizeof(T) == 2)
+    if constexpr (W)
         if (chunks > 2048)
-            return launch_res_norm_cfg<T, MX4, 8, 512, false>(p, sms, st);
-    return launch_res_norm_cfg<T, MX4, 4, 512, false>(p, sms, st);
+            return launch_res_norm_cfg<T, MX4, 8, 512, false, 1>(p, sms, st);
+    return launch_res_norm_cfg<T, MX4, 4, 512, false, 1>(p, sms, st);
 }
 
 // gate_tokens: tokens that share a gate row; gate and gamma may be NULL

@@ -84,10 +84,10 @@ __device__ __forceinline__ double res_squares(const float (&v)[8])
 }
 
 // 1 / RMS from a row's sum of squares: every thread's `s` summed over the
-// block.  `buf` [32] doubles; `out` one float; buf and out are free again after
-// the caller's next barrier.
+// block.  One barrier: each warp adds the warps' sums from `buf` [32] by itself.
+// buf is written again at the earliest two calls later (the caller alternates).
 template <int THREADS>
-__device__ __forceinline__ float res_rinv(double s, double inv_k, float eps, double *buf, volatile float *out)
+__device__ __forceinline__ float res_rinv(double s, double inv_k, float eps, double *buf)
 {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
@@ -96,17 +96,12 @@ __device__ __forceinline__ float res_rinv(double s, double inv_k, float eps, dou
     if (lane == 0)
         buf[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-        double t = lane < THREADS / 32 ? buf[lane] : 0.0;
+    double t = buf[lane & (THREADS / 32 - 1)];
 #pragma unroll
-        for (int d = THREADS / 64; d > 0; d >>= 1)
-            t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
-        const double ms = t * inv_k + static_cast<double>(eps);
-        if (lane == 0)
-            *out = ms > 0.0 ? static_cast<float>(rsqrt(ms)) : (ms == 0.0 ? 0.0f : static_cast<float>(ms));
-    }
-    __syncthreads();
-    return *out;
+    for (int d = THREADS / 64; d > 0; d >>= 1)
+        t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+    const double ms = t * inv_k + static_cast<double>(eps);
+    return ms > 0.0 ? static_cast<float>(rsqrt(ms)) : (ms == 0.0 ? 0.0f : static_cast<float>(ms));
 }
 
 template <int THREADS>
@@ -151,46 +146,50 @@ struct ResArgs {
 };
 
 // CH: chunks of 8 values a thread holds (K <= 8 * CH * THREADS); CACHE: gamma and
-// g in shared memory.
-template <typename T, bool MX4, int CH, int THREADS, bool CACHE>
-__global__ void __launch_bounds__(THREADS) res_norm_kernel(const ResArgs p)
+// g in shared memory, BLOCKS: CTAs an SM holds.
+template <typename T, bool MX4, int CH, int THREADS, bool CACHE, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) res_norm_kernel(const ResArgs p)
 {
     pdl_prologue();
     extern __shared__ float factors[];  // [2][K] with CACHE
-    __shared__ double sum_b[32], sum_r[32];
-    __shared__ float rinv_b, rinv_r, top_s[32];
-    constexpr bool AHEAD = CACHE && CH * sizeof(T) <= 8;  // the next row's loads in flight (registers allow)
-    const int64_t K = p.K, KT = (K + 127) >> 7;
+    __shared__ double sums[2][2][32];   // [row parity][norm][warp]
+    __shared__ float top_s[32];
+    constexpr bool AHEAD = CACHE && CH * sizeof(T) <= 4;  // the next row's loads in flight (registers allow)
+    const int K = static_cast<int>(p.K), KT = (K + 127) >> 7;
     const double inv_k = 1.0 / static_cast<double>(K);
     const T *b = static_cast<const T *>(p.b), *r = static_cast<const T *>(p.r), *gate = static_cast<const T *>(p.gate);
     T *r_out = static_cast<T *>(p.r_out);
-    auto chunk = [&](int i) { return static_cast<int64_t>(i) * THREADS + threadIdx.x; };
+    const bool post = p.gamma != nullptr;
+    int col[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+        col[i] = (i * THREADS + static_cast<int>(threadIdx.x)) * 8;
 
     if constexpr (CACHE) {
-        for (int64_t k = threadIdx.x * 4; k < K; k += THREADS * 4) {
-            if (p.gamma != nullptr)
+        for (int k = threadIdx.x * 4; k < K; k += THREADS * 4) {
+            if (post)
                 *reinterpret_cast<float4 *>(factors + k) = __ldg(reinterpret_cast<const float4 *>(p.gamma + k));
             *reinterpret_cast<float4 *>(factors + K + k) = __ldg(reinterpret_cast<const float4 *>(p.g + k));
         }
         __syncthreads();
     }
-    auto factor = [&](const float *global, int64_t at, int64_t col, float (&f)[8]) {
+    auto factor = [&](const float *global, int at, int c, float (&f)[8]) {
         if constexpr (CACHE) {
-            const float4 x = *reinterpret_cast<const float4 *>(factors + at + col);
-            const float4 y = *reinterpret_cast<const float4 *>(factors + at + col + 4);
+            const float4 x = *reinterpret_cast<const float4 *>(factors + at + c);
+            const float4 y = *reinterpret_cast<const float4 *>(factors + at + c + 4);
             f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
         } else {
-            load8<float>(global + col, f);
+            load8<float>(global + c, f);
         }
     };
     ResRaw<T> bv[CH], rv[CH], bn[AHEAD ? CH : 1], rn[AHEAD ? CH : 1];
     auto fetch = [&](int64_t m, ResRaw<T> *x, ResRaw<T> *y) {
+        const T *pb = b + m * K, *pr = r + m * K;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int64_t col = chunk(i) * 8;
-            if (col < K && m < p.M) {
-                res_load(x[i], b + m * K + col);
-                res_load(y[i], r + m * K + col);
+            if (col[i] < K && m < p.M) {
+                res_load(x[i], pb + col[i]);
+                res_load(y[i], pr + col[i]);
             } else {
                 res_zero(x[i]);
                 res_zero(y[i]);
@@ -199,7 +198,8 @@ __global__ void __launch_bounds__(THREADS) res_norm_kernel(const ResArgs p)
     };
     if constexpr (AHEAD)
         fetch(blockIdx.x, bn, rn);
-    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    int parity = 0;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x, parity ^= 1) {
         if constexpr (AHEAD) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(THREADS) res_norm_kernel(const ResArgs p)
             fetch(m, bv, rv);
         }
         float rb = 0.0f;
-        if (p.gamma != nullptr) {
+        if (post) {
             double s = 0.0;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -219,84 +219,90 @@ __global__ void __launch_bounds__(THREADS) res_norm_kernel(const ResArgs p)
                 res_values(bv[i], v);
                 s += res_squares(v);
             }
-            rb = res_rinv<THREADS>(s, inv_k, p.eps, sum_b, &rinv_b);
+            rb = res_rinv<THREADS>(s, inv_k, p.eps, sums[parity][0]);
         }
         const T *gr = gate == nullptr ? nullptr : gate + (m / p.gate_tokens) * K;
+        T *po = r_out + m * K;
         double s = 0.0;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int64_t col = chunk(i) * 8;
-            if (col >= K)
+            if (col[i] >= K)
                 continue;
             float u[8], f[8], o[8];
             res_values(bv[i], u);
-            if (p.gamma != nullptr) {
-                factor(p.gamma, 0, col, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    u[j] = __fmul_rn(__fmul_rn(u[j], rb), f[j]);
+            if (post) {
+                factor(p.gamma, 0, col[i], f);
+                mul8(u, rb);
+                mul8(u, f);
             }
             if (gr != nullptr) {
-                load8<T>(gr + col, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    u[j] = __fmul_rn(u[j], f[j]);
+                load8<T>(gr + col[i], f);
+                mul8(u, f);
             }
             res_values(rv[i], o);
+            // scalar: a packed product and sum would be fused into one rounding
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 o[j] = __fadd_rn(o[j], __fmul_rn(u[j], p.c));
-            res_store(rv[i], r_out + m * K + col, o);
+            res_store(rv[i], po + col[i], o);
             res_values(rv[i], o);
             s += res_squares(o);
         }
-        const float ra = res_rinv<THREADS>(s, inv_k, p.eps, sum_r, &rinv_r);
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int64_t c8 = chunk(i), col = c8 * 8;
-            const bool in_k = col < K;
-            float a[8], f[8];
+        const float ra = res_rinv<THREADS>(s, inv_k, p.eps, sums[parity][1]);
+        auto scaled = [&](int i, float (&a)[8]) {
+            float f[8];
             res_values(rv[i], a);
-            if (in_k) {
-                factor(p.g, K, col, f);
+            factor(p.g, K, col[i], f);
+            mul8(a, ra);
+            mul8(a, f);
+        };
+        if constexpr (MX4) {
+            uint8_t *pq = p.q + m * (K / 2);
+            uint8_t *ps = static_cast<uint8_t *>(p.sx) + mx4_scale_word(m, 0, KT);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    a[j] = __fmul_rn(__fmul_rn(a[j], ra), f[j]);
-            }
-            if constexpr (MX4) {
-                const int64_t kt = c8 >> 4;
-                if (__ballot_sync(0xFFFFFFFFu, kt < KT) != 0u)  // a whole warp behind the last scale tile has nothing to do
-                    mx4_store_chunk(a, in_k, reinterpret_cast<uint32_t *>(p.q + m * (K / 2) + c8 * 4),
-                                    (threadIdx.x & 15) == 0 && kt < KT
-                                        ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.sx) + mx4_scale_word(m, kt, KT))
-                                        : nullptr);
-            } else if (in_k) {
+            for (int i = 0; i < CH; ++i) {
+                const int kt = col[i] >> 7;
+                if (__ballot_sync(0xFFFFFFFFu, kt < KT) == 0u)  // a whole warp behind the last scale tile has nothing to do
+                    continue;
+                const bool in_k = col[i] < K;
+                float a[8];
+                if (in_k) {
+                    scaled(i, a);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    top = fmaxf(top, fabsf(a[j]));
+                    for (int j = 0; j < 8; ++j)
+                        a[j] = 0.0f;
+                }
+                mx4_store_chunk(a, in_k, reinterpret_cast<uint32_t *>(pq + col[i] / 2),
+                                (threadIdx.x & 15) == 0 && kt < KT
+                                    ? reinterpret_cast<uint32_t *>(ps + static_cast<int64_t>(kt) * kMx4TileBytes)
+                                    : nullptr);
             }
-        }
-        if constexpr (!MX4) {
+        } else {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                if (col[i] < K) {
+                    float a[8];
+                    scaled(i, a);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        top = fmaxf(top, fabsf(a[j]));
+                }
             top = res_max<THREADS>(top, top_s);
             const float sx = __fdiv_rn(top, 127.0f);
             const bool exact = sx < 1e-30f;
             const float inv = exact ? 0.0f : __frcp_rn(sx);
             if (threadIdx.x == 0)
                 static_cast<float *>(p.sx)[m] = sx;
+            uint8_t *pq = p.q + m * K;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int64_t col = chunk(i) * 8;
-                if (col >= K)
-                    continue;
-                float a[8], f[8];
-                res_values(rv[i], a);
-                factor(p.g, K, col, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    a[j] = __fmul_rn(__fmul_rn(a[j], ra), f[j]);
-                *reinterpret_cast<uint2 *>(p.q + m * K + col) = res_int8(a, sx, inv, exact);
-            }
+            for (int i = 0; i < CH; ++i)
+                if (col[i] < K) {
+                    float a[8];
+                    scaled(i, a);
+                    *reinterpret_cast<uint2 *>(pq + col[i]) = res_int8(a, sx, inv, exact);
+                }
         }
     }
     if constexpr (MX4)
