@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 const uint32_t t0 = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage);
                 const uint32_t w_at = static_cast<uint32_t>(stage * (Cfg::W_BYTES >> 4));
                 const uint64_t x = x_desc + static_cast<uint32_t>(stage * (Cfg::X_BYTES >> 4));
-                mx4_stage_mma<BNX>(leader, d, g_desc + w_at, x, t0, t0 + 16, steps_of(kb), kb == 0);
-                mx4_stage_mma<BNX>(leader, d + BNX, u_desc + w_at, x, t0 + 8, t0 + 16, steps_of(kb), kb == 0);
+                mx4_stage_mma<BNX, 1>(leader, d, g_desc + w_at, x, t0, t0 + 16, steps_of(kb), kb == 0);
+                mx4_stage_mma<BNX, 1>(leader, d + BNX, u_desc + w_at, x, t0 + 8, t0 + 16, steps_of(kb), kb == 0);
                 mma_issued_any = true;
                 mma_commit_warp(leader, empty_bar(stage));
                 if (++stage == STAGES) {

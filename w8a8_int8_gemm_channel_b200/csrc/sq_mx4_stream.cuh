@@ -53,7 +53,9 @@ struct Mx4StreamCfg {
     static constexpr int S_BYTES = 2 * kMx4TileBytes;  // scale tiles of one operand's stage
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * S_BYTES;
     static constexpr int MAX_STAGES = BNX == 128 ? 6 : 8;
-    static constexpr int TMEM_COLS = pow2_at_least(2 * BNX + 16 * MAX_STAGES, 32);
+    static constexpr int NACC = BNX == 32 ? 4 : (BNX == 64 ? 2 : 1);  // accumulators a tile rotates over
+    static constexpr int SCALE_COL = 2 * NACC * BNX;                 // two sets of them, then the scales
+    static constexpr int TMEM_COLS = pow2_at_least(SCALE_COL + 16 * MAX_STAGES, 32);
     static_assert(TMEM_COLS <= 512, "TMEM");
 };
 
@@ -112,17 +114,45 @@ __device__ __forceinline__ void mx4_copy_scales(uint32_t taddr, uint32_t saddr, 
 }
 
 // The MMAs of one stage (a whole warp calls; a, b: descriptors of the stage's
-// operands, ta, tb: their scales in TMEM).
-template <int N>
+// operands, ta, tb: their scales in TMEM), over NACC accumulators `stride`
+// columns apart in turn: an MMA of few columns is over long before its sum may be
+// added to again.
+template <int N, int NACC>
 __device__ __forceinline__ void mx4_stage_mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t ta,
-                                              uint32_t tb, int steps, bool first)
+                                              uint32_t tb, int steps, bool first, uint32_t stride = N)
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (k < steps)
-            mma_mx4_warp(leader, d, a + 2 * k, b + 2 * k, (k & 1) ? idesc_mx4(128, N, 2) : idesc_mx4(128, N, 0),
-                         ta + 4 * (k >> 1), tb + 4 * (k >> 1), (first && k == 0) ? 0u : 1u);
+            mma_mx4_warp(leader, d + (k % NACC) * stride, a + 2 * k, b + 2 * k,
+                         (k & 1) ? idesc_mx4(128, N, 2) : idesc_mx4(128, N, 0), ta + 4 * (k >> 1), tb + 4 * (k >> 1),
+                         (first && k < NACC) ? 0u : 1u);
 }
+
+// Where a unit lies: tile, expert (its place in the list) and k block.  Made
+// once for the first unit of a range and stepped from there: dividing 64-bit
+// unit numbers in the producer's loop took it longer than the loads (32 x 28672
+// x 4096: 350 ns a unit with nothing else in the loops).
+struct Mx4Unit {
+    int t, g, kb;
+    __device__ __forceinline__ Mx4Unit(int64_t u, int64_t per_tile, int KB)
+    {
+        t = static_cast<int>(u / per_tile);
+        const int r = static_cast<int>(u - t * per_tile);
+        g = r / KB;
+        kb = r - g * KB;
+    }
+    __device__ __forceinline__ void next(int KB, int G)
+    {
+        if (++kb == KB) {
+            kb = 0;
+            if (++g == G) {
+                g = 0;
+                ++t;
+            }
+        }
+    }
+};
 
 // The weight side of a launch.  Linear: G = 1, one matrix.  Experts: the group
 // list is made in the kernel from ids.
@@ -225,41 +255,39 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            // coordinates of unit u: k block, weight row, scale row tile, token row, token scale row tile
-            auto load_w = [&](int64_t u, int stage) {
-                const int64_t t = u / per_tile;
-                const int r = static_cast<int>(u - t * per_tile);
-                const int g = r / KB, kb = r - g * KB;
-                const int e = MOE ? e_list[g] : 0;
-                tma_load_2d(sW + stage * Cfg::W_BYTES, &tmW, full_bar(stage), kb * 128,
-                            e * N + static_cast<int>(t) * 128);
-                tma_load_3d(sSW + stage * Cfg::S_BYTES, &tmSW, full_bar(stage), 0, kb * 2, e * T + static_cast<int>(t));
+            auto load_w = [&](const Mx4Unit &c, int stage) {
+                const int e = MOE ? e_list[c.g] : 0;
+                tma_load_2d(sW + stage * Cfg::W_BYTES, &tmW, full_bar(stage), c.kb * 128, e * N + c.t * 128);
+                tma_load_3d(sSW + stage * Cfg::S_BYTES, &tmSW, full_bar(stage), 0, c.kb * 2, e * T + c.t);
             };
-            auto load_x = [&](int64_t u, int stage) {
-                const int r = static_cast<int>(u % per_tile);
-                const int g = r / KB, kb = r - g * KB;
-                tma_load_2d(sX + stage * Cfg::X_BYTES, &tmX, full_bar(stage), kb * 128, MOE ? g * M : 0);
-                tma_load_3d(sSX + stage * Cfg::S_BYTES, &tmSX, full_bar(stage), 0, kb * 2, g);
+            auto load_x = [&](const Mx4Unit &c, int stage) {
+                tma_load_2d(sX + stage * Cfg::X_BYTES, &tmX, full_bar(stage), c.kb * 128, MOE ? c.g * M : 0);
+                tma_load_3d(sSX + stage * Cfg::S_BYTES, &tmSX, full_bar(stage), 0, c.kb * 2, c.g);
             };
-            const int64_t nu = u1 - u0;
-            const int pre = pre_wait ? static_cast<int>(nu < stages ? nu : stages) : 0;
+            Mx4Unit w(works ? u0 : 0, max(per_tile, int64_t{1}), KB), x = w;
+            const int nu = static_cast<int>(u1 - u0);
+            const int pre = pre_wait ? min(nu, stages) : 0;
             for (int i = 0; i < pre; ++i) {
                 mbar_arrive_expect_tx(full_bar(i), Cfg::STAGE_BYTES);
-                load_w(u0 + i, i);
+                load_w(w, i);
+                w.next(KB, G);
                 issued_mask |= 1u << i;
             }
             if (pre_wait)
                 asm volatile("griddepcontrol.wait;" ::: "memory");
-            for (int i = 0; i < pre; ++i)
-                load_x(u0 + i, i);
-            int stage = pre % stages;
+            for (int i = 0; i < pre; ++i) {
+                load_x(x, i);
+                x.next(KB, G);
+            }
+            int stage = pre == stages ? 0 : pre;
             uint32_t phase = (pre == stages) ? 1u : 0u;
-            for (int64_t u = u0 + pre; u < u1; ++u) {
+            for (int i = pre; i < nu; ++i) {
                 if (!bounded_wait(empty_bar(stage), phase ^ 1u, kErrWaitProducer, abort_flag))
                     break;
                 mbar_arrive_expect_tx(full_bar(stage), Cfg::STAGE_BYTES);
-                load_w(u, stage);
-                load_x(u, stage);
+                load_w(w, stage);
+                load_x(w, stage);
+                w.next(KB, G);
                 issued_mask |= 1u << stage;
                 issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == stages) {
@@ -270,22 +298,22 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
         }
     } else if (warp == 1) {
         const uint32_t leader = elect_one();
-        const uint32_t tS = tmem_base + 2 * BNX;  // scales: 16 columns a stage
+        const uint32_t tS = tmem_base + Cfg::SCALE_COL;  // scales: 16 columns a stage
         const uint64_t w_desc = smem_desc_k_sw128(sW), x_desc = smem_desc_k_sw128(sX);
         int stage = 0;
         uint32_t phase = 0;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (int64_t u = u0; u < u1 && ok;) {
+        int left = static_cast<int>(u1 - u0);
+        for (int kb0 = static_cast<int>(u0 % KB); left > 0 && ok; kb0 = 0) {
             // one accumulator: the k blocks of one tile and expert
-            const int kb0 = static_cast<int>(u % KB);
-            const int kb1 = static_cast<int>(min(static_cast<int64_t>(KB), kb0 + (u1 - u)));
-            u += kb1 - kb0;
+            const int kb1 = min(KB, kb0 + left);
+            left -= kb1 - kb0;
             if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
                 break;
             tc_fence_after_sync();
-            const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BNX);
+            const uint32_t d = tmem_base + static_cast<uint32_t>(acc * Cfg::NACC * BNX);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
                     !bounded_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
@@ -295,7 +323,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 __syncwarp();
                 tc_fence_after_sync();
                 const uint32_t t0 = tS + 16u * stage;
-                mx4_stage_mma<BNX>(leader, d, w_desc + static_cast<uint32_t>(stage * (Cfg::W_BYTES >> 4)),
+                mx4_stage_mma<BNX, Cfg::NACC>(leader, d, w_desc + static_cast<uint32_t>(stage * (Cfg::W_BYTES >> 4)),
                                    x_desc + static_cast<uint32_t>(stage * (Cfg::X_BYTES >> 4)), t0, t0 + 8, steps_of(kb),
                                    kb == kb0);
                 mma_issued_any = true;
@@ -314,15 +342,18 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
         }
     } else if (warp == 2) {
         if (lane == 0) {
-            const uint32_t tS = tmem_base + 2 * BNX;
+            const uint32_t tS = tmem_base + Cfg::SCALE_COL;
             int stage = 0, last = -1;
             uint32_t phase = 0, last_phase = 0;
-            for (int64_t u = u0; u < u1; ++u) {
+            int kb = static_cast<int>(u0 % KB);
+            for (int left = static_cast<int>(u1 - u0); left > 0; --left) {
                 if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag))
                     break;
                 tc_fence_after_sync();
                 const uint32_t t0 = tS + 16u * stage;
-                const int steps = steps_of(static_cast<int>(u % KB));
+                const int steps = steps_of(kb);
+                if (++kb == KB)
+                    kb = 0;
                 mx4_copy_scales(t0, sSW + stage * Cfg::S_BYTES, steps);
                 mx4_copy_scales(t0 + 8, sSX + stage * Cfg::S_BYTES, steps);
                 mma_commit(scale_bar(stage));
@@ -404,7 +435,8 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 __syncwarp();
                 tc_fence_after_sync();
                 const uint32_t lane_addr =
-                    tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BNX);
+                    tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * Cfg::NACC * BNX);
+                const int parts = min(Cfg::NACC, steps_of(kb0));  // accumulators the first k block set
 #pragma unroll
                 for (int cc = 0; cc < BNX / 32; ++cc) {
                     const uint32_t m = MOE ? wt_mask[wb * 4 + cc] : 0u;
@@ -413,6 +445,15 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(lane_addr + cc * 32, r);
                     tmem_ld_wait();
+#pragma unroll 1
+                    for (int a = 1; a < parts; ++a) {
+                        uint32_t q[32];
+                        tmem_ld_32x32b_x32(lane_addr + static_cast<uint32_t>(a * BNX) + cc * 32, q);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(q[j]));
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         if constexpr (MOE) {
