@@ -163,7 +163,7 @@ __device__ __forceinline__ void mx4_zero_pad(uint8_t *scales, int64_t rows, int6
 // 16, and 256 / TX rows at a time.  Memory-bound: 2 or 4 bytes in and 17/32 out
 // a value; the smoothing divides by multiplying with RN(1 / s), one division a
 // column and band instead of one a value.
-// `zero`: counters of the GEMM after it, cleared on the side.
+// `zero`: tile counts of the product after it, cleared on the side.
 template <typename T, int OP>
 __global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restrict__ x, int64_t rows, int64_t K,
                                                                 const float *__restrict__ s,

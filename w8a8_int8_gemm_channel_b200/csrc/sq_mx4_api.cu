@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -75,7 +76,7 @@ inline Mx4Walk mx4_walk(int64_t rows, int64_t K, int64_t sms)
 
 template <typename T>
 sq_status launch_mx4_quant(const T *x, int64_t rows, int64_t K, const float *s, int op, uint8_t *q, uint8_t *sc,
-                           cudaStream_t st, int *zero = nullptr, int nzero = 0)
+                           cudaStream_t st, int *zero, int nzero)
 {
     DeviceInfo di;
     if (!device_info(di))
@@ -131,26 +132,46 @@ bool make_tmap_scales(CUtensorMap *map, const uint8_t *scales, int64_t row_tiles
     return r == CUDA_SUCCESS;
 }
 
-constexpr int64_t kMx4MaxCtas = 160;  // of the streaming kernel: at least the SM count of every sm_100 part
+using sq::kMx4MaxCtas;
 
 inline int mx4_bnx(int64_t M) { return M <= 32 ? 32 : (M <= 64 ? 64 : 128); }
 
-// Workspace of the product for few tokens: a counter for each tile of 128
-// channels, then two partial tiles a CTA.  More tokens need none.
+// A number for each call that no other call has, its lower 16 bits 0: the tile
+// counts carry it.  A random start and an odd step, so that what a workspace
+// happens to hold does not match.
+unsigned long long next_call_number()
+{
+    static std::atomic<unsigned long long> n{[] {
+        unsigned long long v = static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count());
+        v ^= reinterpret_cast<uintptr_t>(&v) << 20;
+        return v * 0x9E3779B97F4A7C15ull;
+    }()};
+    unsigned long long v;
+    do
+        v = n.fetch_add(0x9E3779B97F4A7C15ull) << 16;
+    while (v == 0);
+    return v;
+}
+
+constexpr size_t kMx4Words = kMx4MaxCtas * sizeof(unsigned long long);  // a tagged tile count for each CTA
+constexpr size_t kMx4Counts = kMx4MaxCtas * sizeof(int);                // a plain one
+
+// Workspace of the product for few tokens: the tile counts, then two partial
+// tiles a CTA.  More tokens need none.
 struct Mx4Ws {
     size_t cnt = 0, slots = 0, total = 0;
-    int ncnt = 0;
+    bool few = false;
 };
 
-inline Mx4Ws mx4_ws(int64_t M, int64_t N, size_t base)
+inline Mx4Ws mx4_ws(int64_t M, size_t base)
 {
     Mx4Ws w;
     w.total = base;
     if (M > sq::kMx4MaxTokens)
         return w;
-    w.ncnt = static_cast<int>((N + 127) / 128);
+    w.few = true;
     w.cnt = base;
-    w.slots = base + round256(static_cast<size_t>(w.ncnt) * sizeof(int));
+    w.slots = base + round256(kMx4Counts);
     w.total = w.slots + static_cast<size_t>(kMx4MaxCtas) * 2 * mx4_bnx(M) * 128 * sizeof(float);
     return w;
 }
@@ -180,8 +201,8 @@ sq_status launch_mx4_stream(const uint8_t *xq, const uint8_t *sx, const uint8_t 
         std::fprintf(stderr, "sq mx4 stream M=%lld N=%lld K=%lld: BNX=%d ctas=%lld stages=%d\n", (long long)M,
                      (long long)N, (long long)K, BNX, (long long)G, stages);
     return launch_kernel(kernel, dim3(static_cast<unsigned>(G)), dim3(sq::kMx4StreamThreads), smem, st, 0, 0, tw, tsw, tx,
-                         tsx, y, slots, cnt, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
-                         static_cast<int>(G), stages, 0, sq::Mx4MoeArgs{});
+                         tsx, y, slots, cnt, static_cast<int>(M), static_cast<int>(N),
+                         static_cast<int>(K), static_cast<int>(G), stages, 0, sq::Mx4MoeArgs{});
 }
 
 template <int BN, int OUT>
@@ -247,7 +268,7 @@ sq_status launch_mx4_pair(const uint8_t *xq, const uint8_t *sx, const uint8_t *w
     }
 }
 
-// cnt: the tile counters, cleared by the kernel right before on the stream
+// cnt: the tile counts, cleared by the kernel right before on the stream
 template <int OUT>
 sq_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M,
                           int64_t N, int64_t K, void *y, int *cnt, float *slots, cudaStream_t st)
@@ -273,7 +294,7 @@ sq_status check_mx4_gemm_dims(int64_t M, int64_t N, int64_t K)
 __global__ void mx4_clear_kernel(int *p, int n)
 {
     sq::pdl_prologue();
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x)
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
         p[i] = 0;
 }
 
@@ -287,28 +308,28 @@ inline Mx4LinearWs mx4_linear_ws(int64_t M, int64_t N, int64_t K)
 {
     Mx4LinearWs w;
     w.sx = round256(static_cast<size_t>(M) * static_cast<size_t>(K / 2));
-    w.g = mx4_ws(M, N, w.sx + scale_bytes(M, K));
+    w.g = mx4_ws(M, w.sx + scale_bytes(M, K));
     return w;
 }
 
 // ---- experts layer for few tokens ------------------------------------------------
 // Workspace: h's codes and scale tiles (a tile per expert in use and 128
-// values), then the down projection's counters and partial tiles.
+// values), the two halves' tile counts, and partial tiles (the first half's, two
+// accumulators each; the second half's are fewer).
 struct Mx4MoeWs {
-    size_t hs = 0, cnt = 0, slots = 0, total = 0;
+    size_t hs = 0, words = 0, cnt = 0, slots = 0, total = 0;
     int64_t groups = 0;  // experts that can be in use at once
-    int ncnt = 0;
 };
 
-inline Mx4MoeWs mx4_moe_ws(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
+inline Mx4MoeWs mx4_moe_ws(int64_t T, int64_t topk, int64_t E, int64_t I)
 {
     Mx4MoeWs w;
     w.groups = std::min(E, T * topk);
     w.hs = round256(static_cast<size_t>(w.groups * T) * static_cast<size_t>(I / 2));
-    w.cnt = w.hs + static_cast<size_t>(w.groups) * scale_bytes(1, I);
-    w.ncnt = static_cast<int>((H + 127) / 128);
-    w.slots = w.cnt + round256(static_cast<size_t>(w.ncnt) * sizeof(int));
-    w.total = w.slots + static_cast<size_t>(kMx4MaxCtas) * 2 * mx4_bnx(T) * 128 * sizeof(float);
+    w.words = w.hs + static_cast<size_t>(w.groups) * scale_bytes(1, I);
+    w.cnt = w.words + round256(kMx4Words);
+    w.slots = w.cnt + round256(kMx4Counts);
+    w.total = w.slots + static_cast<size_t>(kMx4MaxCtas) * 2 * 2 * mx4_bnx(T) * 128 * sizeof(float);
     return w;
 }
 
@@ -321,6 +342,10 @@ sq_status check_mx4_moe_dims(int64_t T, int64_t topk, int64_t E, int64_t H, int6
         return SQ_ERR_UNSUPPORTED;
     return SQ_OK;
 }
+
+// Units (17 KB) of the second half that a CTA of the first prefetches into L2 once
+// its own loads are out: 62 MB in all, half of the L2.
+constexpr int kMx4Ahead = 24;
 
 struct Mx4MoeCall {
     const uint8_t *xq, *sx, *wg, *sg, *wu, *su, *wd, *sd;
@@ -345,20 +370,21 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
     if (!ensure_smem_attr(up, Up::SMEM_BYTES, up_done) || !ensure_smem_attr(down, kMaxDynSmem, down_done))
         return SQ_ERR_CUDA;
     uint8_t *hq = c.ws, *hs = c.ws + c.L.hs;
+    unsigned long long *words = reinterpret_cast<unsigned long long *>(c.ws + c.L.words);
     int *cnt = reinterpret_cast<int *>(c.ws + c.L.cnt);
     float *slots = reinterpret_cast<float *>(c.ws + c.L.slots);
     const int64_t E = c.route.E, RI = (c.I + 127) / 128, RH = (c.H + 127) / 128;
     CUtensorMap tg, tsg, tu, tsu, tx, tsx, td, tsd, th, tsh;
-    if (!make_tmap_mx4(&tg, c.wg, E * c.I, c.H, 32) || !make_tmap_scales(&tsg, c.sg, E * RI, c.H, 1) ||
-        !make_tmap_mx4(&tu, c.wu, E * c.I, c.H, 32) || !make_tmap_scales(&tsu, c.su, E * RI, c.H, 1) ||
+    if (!make_tmap_mx4(&tg, c.wg, E * c.I, c.H, 128) || !make_tmap_scales(&tsg, c.sg, E * RI, c.H, 1) ||
+        !make_tmap_mx4(&tu, c.wu, E * c.I, c.H, 128) || !make_tmap_scales(&tsu, c.su, E * RI, c.H, 1) ||
         !make_tmap_mx4(&tx, c.xq, c.T, c.H, BNX) || !make_tmap_scales(&tsx, c.sx, 1, c.H, 1) ||
         !make_tmap_mx4(&td, c.wd, E * c.H, c.I, 128) || !make_tmap_scales(&tsd, c.sd, E * RH, c.I, 1) ||
         !make_tmap_mx4(&th, hq, c.L.groups * c.T, c.I, BNX) || !make_tmap_scales(&tsh, hs, c.L.groups, c.I, 1))
         return SQ_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(di.sms, kMx4MaxCtas));
     sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), Up::SMEM_BYTES, st, 0, 0,
-                                tg, tsg, tu, tsu, tx, tsx, hq, hs, cnt, c.L.ncnt, static_cast<int>(c.T),
-                                static_cast<int>(c.H), static_cast<int>(c.I), c.route);
+                                tg, tsg, tu, tsu, tx, tsx, td, tsd, hq, hs, slots, words, next_call_number(), cnt, static_cast<int>(c.T),
+                                static_cast<int>(c.H), static_cast<int>(c.I), kMx4Ahead, c.route);
     if (r != SQ_OK)
         return r;
     constexpr int stages = BNX == 128 ? 6 : 8;
@@ -480,7 +506,7 @@ sq_status sq_mx4_dequant(const uint8_t *q, const uint8_t *sc, int64_t rows, int6
 
 size_t sq_mx4_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
 {
-    return check_mx4_gemm_dims(M, N, K) == SQ_OK ? mx4_ws(M, N, 0).total : 0;
+    return check_mx4_gemm_dims(M, N, K) == SQ_OK ? mx4_ws(M, 0).total : 0;
 }
 
 sq_status sq_mx4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, int64_t M, int64_t N,
@@ -491,16 +517,14 @@ sq_status sq_mx4_gemm(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, c
     sq_status r = check_mx4_gemm_dims(M, N, K);
     if (r != SQ_OK)
         return r;
-    const Mx4Ws w = mx4_ws(M, N, 0);
+    const Mx4Ws w = mx4_ws(M, 0);
     if (w.total > 0 && (!ok_ptr(workspace) || ws_bytes < w.total))
         return SQ_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    int *cnt = nullptr;
-    float *slots = nullptr;
-    if (w.total > 0) {
-        cnt = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + w.cnt);
-        slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.slots);
-        r = launch_kernel(mx4_clear_kernel, dim3(1), dim3(256), 0, st, 0, 0, cnt, w.ncnt);
+    int *cnt = w.few ? reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + w.cnt) : nullptr;
+    float *slots = w.few ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.slots) : nullptr;
+    if (w.few) {
+        r = launch_kernel(mx4_clear_kernel, dim3(1), dim3(kMx4MaxCtas), 0, st, 0, 0, cnt, static_cast<int>(kMx4MaxCtas));
         if (r != SQ_OK)
             return r;
     }
@@ -528,10 +552,9 @@ sq_status sq_mx4_linear(const void *x, sq_dtype in_dt, const float *s, const uin
         return SQ_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *xq = static_cast<uint8_t *>(workspace), *sx = xq + L.sx;
-    const bool few = L.g.ncnt > 0;
-    int *cnt = few ? reinterpret_cast<int *>(xq + L.g.cnt) : nullptr;
-    float *slots = few ? reinterpret_cast<float *>(xq + L.g.slots) : nullptr;
-    r = mx4_quant(x, in_dt, M, K, s, sq::MX4_OVER, xq, sx, st, cnt, L.g.ncnt);
+    int *cnt = L.g.few ? reinterpret_cast<int *>(xq + L.g.cnt) : nullptr;
+    float *slots = L.g.few ? reinterpret_cast<float *>(xq + L.g.slots) : nullptr;
+    r = mx4_quant(x, in_dt, M, K, s, sq::MX4_OVER, xq, sx, st, cnt, L.g.few ? static_cast<int>(kMx4MaxCtas) : 0);
     if (r != SQ_OK)
         return r;
     return out_dt == SQ_BF16 ? launch_mx4_gemm<OUT_BF16>(xq, sx, wq, sw, M, N, K, y, cnt, slots, st)
@@ -540,7 +563,7 @@ sq_status sq_mx4_linear(const void *x, sq_dtype in_dt, const float *s, const uin
 
 size_t sq_mx4_moe_workspace_size(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I)
 {
-    return check_mx4_moe_dims(T, topk, E, H, I) == SQ_OK ? mx4_moe_ws(T, topk, E, H, I).total : 0;
+    return check_mx4_moe_dims(T, topk, E, H, I) == SQ_OK ? mx4_moe_ws(T, topk, E, I).total : 0;
 }
 
 sq_status sq_mx4_moe(const uint8_t *xq, const uint8_t *sx, const int32_t *ids, const float *weights, int64_t T,
@@ -554,7 +577,7 @@ sq_status sq_mx4_moe(const uint8_t *xq, const uint8_t *sx, const int32_t *ids, c
     const sq_status r = check_mx4_moe_dims(T, topk, E, H, I);
     if (r != SQ_OK)
         return r;
-    const Mx4MoeWs L = mx4_moe_ws(T, topk, E, H, I);
+    const Mx4MoeWs L = mx4_moe_ws(T, topk, E, I);
     if (!ok_ptr(workspace) || ws_bytes < L.total)
         return SQ_ERR_INVALID_ARG;
     const Mx4MoeCall c{xq, sx, wg, sg, wu, su, wd, sd, {ids, weights, static_cast<int>(topk), static_cast<int>(E)},

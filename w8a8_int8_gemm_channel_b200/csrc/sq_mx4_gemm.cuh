@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kMx4PairThreads, 1)
             uint32_t acc_phase = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
-                if (!bounded_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
+                if (!__all_sync(0xFFFFFFFFu, bounded_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag)))
                     break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(kMx4PairThreads, 1)
                 const uint32_t shift = static_cast<uint32_t>(n_blk * BN % 128 / 32);
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     const int next = stage + 1 == STAGES ? 0 : stage + 1;
-                    if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
-                        !bounded_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                    if (!warp_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
+                        !warp_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
                         ok = false;
                         break;
                     }

@@ -15,15 +15,23 @@
 // weights takes an SM about 700 cycles to stream and the MMAs of 64 columns
 // some 260).  Only the chosen (expert, token) pairs are activated and stored.
 //
-// Work.  A unit is 32 channels of one expert, which is one block of the
-// quantised h, so every unit's scale is made by one warp and no CTA needs
-// another's sums.  The units are cut into equal contiguous ranges, one a CTA; a
-// CTA takes up to four units that lie in one 128-row tile at a time and loads
-// just their rows (the other rows of the MMA tile hold whatever was there: they
-// reach only their own, unread, accumulator rows).
+// Work.  A unit is one 256-value k block of one 128-channel tile of one expert,
+// gate and up together: 32 KB of codes and 2 KB of scales.  The units, tile by
+// tile and expert by expert, are cut into equal contiguous ranges, one a CTA.  (An
+// earlier cut into whole-K items of 32 to 128 channels needed no sums across CTAs
+// but left the CTAs with the narrow items behind: their rings held too few bytes
+// to hide the loaded memory's latency; two experts of 4096 x 14336 took 38 us.)
 //
-// Roles as in mx4_stream_kernel.  The gate and the up product of a unit are two
-// accumulators in the same lanes, so a thread holds both values of its channel.
+// A tile that several CTAs share is summed through the workspace; the last of
+// them (mx4_last_of) adds the partials in the contributors'
+// order, activates and stores.
+//
+// While the last tiles are finished nothing is left to load, so the producer
+// prefetches the first units of this CTA's range of the second half into L2.
+//
+// Roles as in mx4_stream_kernel.  The gate and the up product are two
+// accumulators in the same lanes, so a thread holds both values of its channel,
+// and a warp the 32 channels of one block of the quantised h.
 #pragma once
 
 #include <cstdint>
@@ -45,9 +53,34 @@ struct Mx4UpCfg {
     static constexpr int TMEM_COLS = pow2_at_least(NACC * 2 * BNX + STAGES * SCALE_COLS, 32);
     static constexpr int NUM_BARS = 3 * STAGES + 5;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NUM_BARS * 8 + 24 + 2 * 16 +
-                                      (kMx4MaxExperts / 32) * 4 + kMx4MaxExperts * 2;
+                                      (kMx4MaxExperts / 32) * 4 + kMx4MaxExperts * 2 + kMx4MaxSlots * 2;
     static_assert(TMEM_COLS <= 512 && SMEM_BYTES <= 232448, "limits");
 };
+
+// Counts this CTA in at a shared tile's word and tells whether it is the last of
+// `total`.  The word's upper 48 bits are the call's number, which no other call
+// has, the lower 16 the count: whatever else a word holds counts as none, so a
+// workspace may hold anything, and the last one sets it back to 0, so that a
+// captured call may be replayed.  Release and acquire: the partials written
+// before (ordered by the caller's barrier) are visible to the last one.  (Nothing
+// runs before this kernel to clear a plain count; a plain count is a round trip
+// faster where contributors meet, so the second half uses one that this kernel
+// clears.)
+__device__ __forceinline__ bool mx4_last_of(unsigned long long *word, unsigned long long call, int total)
+{
+    unsigned long long seen = 0, count;
+    for (;;) {
+        count = (seen >> 16) == (call >> 16) ? (seen & 0xFFFFu) + 1 : 1;
+        const unsigned long long old = atom_cas_acq_rel_gpu(word, seen, (call & ~0xFFFFull) | count);
+        if (old == seen)
+            break;
+        seen = old;  // every retry follows another contributor's success: at most `total` of them
+    }
+    if (count != static_cast<unsigned long long>(total))
+        return false;
+    *reinterpret_cast<volatile unsigned long long *>(word) = 0;
+    return true;
+}
 
 // The E2M1 code of one scaled value (bits 0-3).
 __device__ __forceinline__ uint32_t mx4_code1(float v)
@@ -62,13 +95,53 @@ __device__ __forceinline__ uint32_t mx4_code1(float v)
     return d & 0xFu;
 }
 
+// Four tokens (t < 0: none) of every lane's channel: activates, quantises over the
+// 32 lanes and stores codes and scale byte.  Written once and looped over the
+// chosen tokens: unrolled over all of a tile's columns, the instruction fetches
+// took longer than the work.
+__device__ __forceinline__ void mx4_store_h4(const int (&t)[4], const float (&g)[4], const float (&u)[4], uint8_t *codes,
+                                             int row_bytes, uint8_t *scale, int zero_behind)
+{
+    const int lane = threadIdx.x & 31;
+    float h[4];
+    uint32_t byte[4], c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = __fmul_rn(__fdiv_rn(g[i], __fadd_rn(1.0f, expf(-g[i]))), u[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        byte[i] = mx4_scale_byte(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h[i]) & 0x7FFFFFFFu)));
+        c[i] = byte[i] == 255u ? 0u : mx4_code1(h[i] * mx4_inv_scale(byte[i])) << (4 * (lane & 7));
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] |= __shfl_xor_sync(0xFFFFFFFFu, c[i], d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (t[i] < 0)
+            continue;
+        if ((lane & 7) == 0)
+            *reinterpret_cast<uint32_t *>(codes + static_cast<int64_t>(t[i]) * row_bytes + (lane >> 3) * 4) = c[i];
+        if (lane == 0) {
+            uint8_t *s = scale + (t[i] & 31) * 16 + (t[i] >> 5) * 4;
+            *s = static_cast<uint8_t>(byte[i]);
+            for (int p = 1; p <= zero_behind; ++p)
+                s[p] = 0;
+        }
+    }
+}
+
 template <int BNX>
 __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     mx4_moe_up_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmSG,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmSU,
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
-                      uint8_t *__restrict__ hq, uint8_t *__restrict__ hs, int *__restrict__ cnt, int ncnt, int M, int H,
-                      int I, Mx4MoeArgs moe)
+                      const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmSD,
+                      uint8_t *__restrict__ hq, uint8_t *__restrict__ hs, float *__restrict__ ws,
+                      unsigned long long *__restrict__ words, unsigned long long call, int *__restrict__ cnt, int M, int H, int I,
+                      int ahead, Mx4MoeArgs moe)
 {
     using Cfg = Mx4UpCfg<BNX>;
     constexpr int STAGES = Cfg::STAGES;
@@ -93,9 +166,11 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gb + misc_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gb + misc_off + 4);
     volatile int *n_groups = reinterpret_cast<volatile int *>(gb + misc_off + 8);
+    volatile int *last_flag = reinterpret_cast<volatile int *>(gb + misc_off + 12);
     uint32_t *tok_mask = reinterpret_cast<uint32_t *>(gb + misc_off + 24);  // [2][4]
     uint32_t *e_mask = tok_mask + 8;
     uint16_t *e_list = reinterpret_cast<uint16_t *>(e_mask + kMx4MaxExperts / 32);
+    uint16_t *chosen = e_list + kMx4MaxExperts;
 
     if (threadIdx.x == 32) {
         for (int i = 0; i < STAGES; ++i) {
@@ -128,28 +203,18 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     pdl_prologue();
-    const int G = mx4_active_experts(moe.ids, M * moe.topk, moe.E, e_mask, e_list, n_groups);
-    // the second half's tile counters
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < ncnt; i += gridDim.x * blockDim.x)
-        cnt[i] = 0;
-
-    const int IU = I / 32, RT = (I + 127) / 128, KB = (H + kMx4KB - 1) / kMx4KB;
-    const int64_t V = static_cast<int64_t>(G) * IU;
-    const int64_t v0 = dec_start(blockIdx.x, V, gridDim.x), v1 = dec_start(blockIdx.x + 1, V, gridDim.x);
-    // item at unit v: up to four units of one expert's 128-row tile
-    struct Item {
-        int g, tile, sub, nu;
-    };
-    auto item_at = [&](int64_t v) {
-        Item it;
-        it.g = static_cast<int>(v / IU);
-        const int q = static_cast<int>(v - static_cast<int64_t>(it.g) * IU);
-        it.tile = q >> 2;
-        it.sub = q & 3;
-        it.nu = static_cast<int>(min(static_cast<int64_t>(min(4 - it.sub, IU - q)), v1 - v));
-        return it;
-    };
-
+    const int G = mx4_active_experts(moe.ids, M * moe.topk, moe.E, e_mask, e_list, chosen, n_groups);
+    // the second half's tile counts
+    if (threadIdx.x == 0 && blockIdx.x < kMx4MaxCtas)
+        cnt[blockIdx.x] = 0;
+    const int RT = (I + 127) / 128, KB = (H + kMx4KB - 1) / kMx4KB;
+    const int64_t U = static_cast<int64_t>(G) * RT * KB;
+    const int64_t C = min(static_cast<int64_t>(gridDim.x), U);  // CTAs with work
+    const int64_t c = blockIdx.x;
+    const bool works = c < C;
+    const int64_t u0 = works ? dec_start(c, U, C) : 0;
+    const int nu = works ? static_cast<int>(dec_start(c + 1, U, C) - u0) : 0;
+    const Mx4Unit first(u0, static_cast<int64_t>(RT) * KB, KB);  // t: expert's place in the list, g: its tile
     auto steps_of = [&](int kb) { return min(4, (H - kb * kMx4KB + 63) >> 6); };
     uint32_t issued_mask = 0, issued_parity = 0;
     bool mma_issued_any = false;
@@ -158,34 +223,38 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int64_t v = v0; v < v1 && ok;) {
-                const Item it = item_at(v);
-                v += it.nu;
-                const int e = e_list[it.g];
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!bounded_wait(empty_bar(stage), phase ^ 1u, kErrWaitProducer, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = full_bar(stage);
-                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(it.nu * 2 * 4096 + Cfg::X_BYTES + 3 * Cfg::S_BYTES));
-                    const uint32_t s0 = sS + stage * 3 * Cfg::S_BYTES;
-                    for (int q = it.sub; q < it.sub + it.nu; ++q) {
-                        const int r = e * I + it.tile * 128 + q * 32;
-                        tma_load_2d(sG + stage * Cfg::W_BYTES + q * 4096, &tmG, fb, kb * 128, r);
-                        tma_load_2d(sU + stage * Cfg::W_BYTES + q * 4096, &tmU, fb, kb * 128, r);
-                    }
-                    tma_load_3d(s0, &tmSG, fb, 0, kb * 2, e * RT + it.tile);
-                    tma_load_3d(s0 + Cfg::S_BYTES, &tmSU, fb, 0, kb * 2, e * RT + it.tile);
-                    tma_load_2d(sX + stage * Cfg::X_BYTES, &tmX, fb, kb * 128, 0);
-                    tma_load_3d(s0 + 2 * Cfg::S_BYTES, &tmSX, fb, 0, kb * 2, 0);
-                    issued_mask |= 1u << stage;
-                    issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+            Mx4Unit w = first;
+            for (int i = 0; i < nu; ++i) {
+                if (!bounded_wait(empty_bar(stage), phase ^ 1u, kErrWaitProducer, abort_flag))
+                    break;
+                const uint32_t fb = full_bar(stage);
+                mbar_arrive_expect_tx(fb, Cfg::STAGE_BYTES);
+                const int e = e_list[w.t];
+                const uint32_t s0 = sS + stage * 3 * Cfg::S_BYTES;
+                tma_load_2d(sG + stage * Cfg::W_BYTES, &tmG, fb, w.kb * 128, e * I + w.g * 128);
+                tma_load_2d(sU + stage * Cfg::W_BYTES, &tmU, fb, w.kb * 128, e * I + w.g * 128);
+                tma_load_3d(s0, &tmSG, fb, 0, w.kb * 2, e * RT + w.g);
+                tma_load_3d(s0 + Cfg::S_BYTES, &tmSU, fb, 0, w.kb * 2, e * RT + w.g);
+                tma_load_2d(sX + stage * Cfg::X_BYTES, &tmX, fb, w.kb * 128, 0);
+                tma_load_3d(s0 + 2 * Cfg::S_BYTES, &tmSX, fb, 0, w.kb * 2, 0);
+                w.next(KB, RT);
+                issued_mask |= 1u << stage;
+                issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            // the down projection's units, as mx4_stream_kernel cuts them
+            const int T = (H + 127) / 128, KBD = (I + kMx4KB - 1) / kMx4KB;
+            const int64_t UD = static_cast<int64_t>(G) * T * KBD, CD = min(static_cast<int64_t>(gridDim.x), UD);
+            if (c < CD && !*abort_flag) {
+                const int64_t d0 = dec_start(c, UD, CD);
+                Mx4Unit d(d0, static_cast<int64_t>(G) * KBD, KBD);
+                for (int i = static_cast<int>(min(dec_start(c + 1, UD, CD) - d0, static_cast<int64_t>(ahead))); i > 0; --i) {
+                    tma_prefetch_l2_2d(&tmD, d.kb * 128, e_list[d.g] * H + d.t * 128);
+                    tma_prefetch_l2_3d(&tmSD, 0, d.kb * 2, e_list[d.g] * T + d.t);
+                    d.next(KBD, G);
                 }
             }
         }
@@ -198,15 +267,17 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (int64_t v = v0; v < v1 && ok;) {
-            v += item_at(v).nu;
-            if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
+        int left = nu;
+        for (int kb0 = first.kb; left > 0 && ok; kb0 = 0) {
+            const int kb1 = min(KB, kb0 + left);
+            left -= kb1 - kb0;
+            if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
                 break;
             tc_fence_after_sync();
             const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 2 * BNX);
-            for (int kb = 0; kb < KB; ++kb) {
-                if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
-                    !bounded_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!warp_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
+                    !warp_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -215,8 +286,8 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 const uint32_t t0 = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage);
                 const uint32_t w_at = static_cast<uint32_t>(stage * (Cfg::W_BYTES >> 4));
                 const uint64_t x = x_desc + static_cast<uint32_t>(stage * (Cfg::X_BYTES >> 4));
-                mx4_stage_mma<BNX, 1>(leader, d, g_desc + w_at, x, t0, t0 + 16, steps_of(kb), kb == 0);
-                mx4_stage_mma<BNX, 1>(leader, d + BNX, u_desc + w_at, x, t0 + 8, t0 + 16, steps_of(kb), kb == 0);
+                mx4_stage_mma<BNX, 1>(leader, d, g_desc + w_at, x, t0, t0 + 16, steps_of(kb), kb == kb0);
+                mx4_stage_mma<BNX, 1>(leader, d + BNX, u_desc + w_at, x, t0 + 8, t0 + 16, steps_of(kb), kb == kb0);
                 mma_issued_any = true;
                 mma_commit_warp(leader, empty_bar(stage));
                 if (++stage == STAGES) {
@@ -237,27 +308,25 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             const uint32_t tS = tmem_base + Cfg::NACC * 2 * BNX;
             int stage = 0, last = -1;
             uint32_t phase = 0, last_phase = 0;
-            bool ok = true;
-            for (int64_t v = v0; v < v1 && ok;) {
-                v += item_at(v).nu;
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t t0 = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage);
-                    const uint32_t s0 = sS + stage * 3 * Cfg::S_BYTES;
-                    mx4_copy_scales(t0, s0, steps_of(kb));
-                    mx4_copy_scales(t0 + 8, s0 + Cfg::S_BYTES, steps_of(kb));
-                    mx4_copy_scales(t0 + 16, s0 + 2 * Cfg::S_BYTES, steps_of(kb));
-                    mma_commit(scale_bar(stage));
-                    last = stage;
-                    last_phase = phase;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+            int kb = first.kb;
+            for (int left = nu; left > 0; --left) {
+                if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag))
+                    break;
+                tc_fence_after_sync();
+                const uint32_t t0 = tS + static_cast<uint32_t>(Cfg::SCALE_COLS * stage);
+                const uint32_t s0 = sS + stage * 3 * Cfg::S_BYTES;
+                const int steps = steps_of(kb);
+                if (++kb == KB)
+                    kb = 0;
+                mx4_copy_scales(t0, s0, steps);
+                mx4_copy_scales(t0 + 8, s0 + Cfg::S_BYTES, steps);
+                mx4_copy_scales(t0 + 16, s0 + 2 * Cfg::S_BYTES, steps);
+                mma_commit(scale_bar(stage));
+                last = stage;
+                last_phase = phase;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
             // the last copies have landed before the CTA may release TMEM
@@ -265,70 +334,81 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 bounded_wait(scale_bar(last), last_phase, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
         }
     } else {
-        // epilogue warps 3..6: warp w holds unit w % 4 of the tile, a channel a lane
+        // epilogue warps 3..6: warp w holds block w % 4 of the tile, a channel a lane
         const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
         const int et = threadIdx.x - 96;
+        constexpr int SLOT = 2 * BNX * 128;  // floats of a partial tile: [gate, up][token][row]
         int acc = 0, wb = 0;
         uint32_t acc_phase = 0;
-        for (int64_t v = v0; v < v1;) {
-            const Item it = item_at(v);
-            v += it.nu;
+        Mx4Unit w = first;
+        for (int left = nu; left > 0;) {
+            const int g = w.t, tile = w.g, kb0 = w.kb, kb1 = min(KB, kb0 + left);
+            const bool whole = kb0 == 0 && kb1 == KB;
+            left -= kb1 - kb0;
+            w.kb = KB - 1;
+            w.next(KB, RT);
             {
                 // the tokens that chose this expert
-                const int e = e_list[it.g];
+                const int e = e_list[g];
                 bool has = false;
                 if (et < M)
                     for (int k = 0; k < moe.topk; ++k)
-                        has = has || __ldg(moe.ids + et * moe.topk + k) == e;
+                        has = has || chosen[et * moe.topk + k] == e;
                 const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
                 if (lane == 0)
                     tok_mask[wb * 4 + (et >> 5)] = m;
                 dec_bar_sync();
             }
+            const uint32_t *mask = tok_mask + wb * 4;
+            wb ^= 1;
             // as in mx4_stream_kernel, a wait that gives up lets the warps go on
             bounded_wait(tfull_bar(acc), acc_phase, kErrWaitAccFull, abort_flag);
             __syncwarp();
             tc_fence_after_sync();
-            if (quarter >= it.sub && quarter < it.sub + it.nu) {
-                const int unit = it.tile * 4 + quarter;
-                const uint32_t lane_addr =
-                    tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 2 * BNX);
-                uint8_t *srow = hs + (static_cast<int64_t>(it.g) * RT + it.tile) * kMx4TileBytes + quarter;
-#pragma unroll 1
-                for (int cc = 0; cc < BNX / 32; ++cc) {
-                    const uint32_t m = tok_mask[wb * 4 + cc];
-                    if (m == 0u)
-                        continue;
-                    uint32_t a[32], b[32];
-                    tmem_ld_32x32b_x32(lane_addr + cc * 32, a);
-                    tmem_ld_32x32b_x32(lane_addr + BNX + cc * 32, b);
-                    tmem_ld_wait();
+            const int unit = tile * 4 + quarter;
+            const bool inside = unit * 32 < I;
+            const int zero_behind = (unit + 1) * 32 == I ? 3 - quarter : 0;  // padding blocks of the last tile
+            uint8_t *codes = hq + static_cast<int64_t>(g) * M * (I / 2) + unit * 16;
+            uint8_t *scale = hs + (static_cast<int64_t>(g) * RT + tile) * kMx4TileBytes + quarter;
+            float *mine = ws + (c * 2 + (g == first.t && tile == first.g ? 0 : 1)) * SLOT;
+            const uint32_t lane_addr =
+                tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 2 * BNX);
+            // four chosen tokens at a time
+            auto take4 = [](uint32_t &m, int cc, int (&t)[4]) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (!(m & (1u << j)))
-                            continue;
-                        const float gv = __uint_as_float(a[j]);
-                        const float h = __fmul_rn(__fdiv_rn(gv, __fadd_rn(1.0f, expf(-gv))), __uint_as_float(b[j]));
-                        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
-                        const uint32_t byte = mx4_scale_byte(__uint_as_float(top));
-                        uint32_t c = byte == 255u ? 0u : mx4_code1(h * mx4_inv_scale(byte)) << (4 * (lane & 7));
-                        c |= __shfl_xor_sync(0xFFFFFFFFu, c, 1);
-                        c |= __shfl_xor_sync(0xFFFFFFFFu, c, 2);
-                        c |= __shfl_xor_sync(0xFFFFFFFFu, c, 4);
-                        const int64_t t = static_cast<int64_t>(it.g) * M + cc * 32 + j;
-                        if ((lane & 7) == 0)
-                            *reinterpret_cast<uint32_t *>(hq + t * (I / 2) + unit * 16 + (lane >> 3) * 4) = c;
-                        if (lane == 0) {
-                            uint8_t *s = srow + j * 16 + cc * 4;
-                            *s = static_cast<uint8_t>(byte);
-                            if (unit == IU - 1)  // the blocks behind the last one hold 0
-                                for (int p = 1; p < 4 - quarter; ++p)
-                                    s[p] = 0;
+                for (int i = 0; i < 4; ++i) {
+                    t[i] = m != 0u ? cc * 32 + __ffs(m) - 1 : -1;
+                    m &= m - 1;
+                }
+            };
+            if (inside) {
+#pragma unroll 1
+                for (int cc = 0; cc < BNX / 32; ++cc)
+#pragma unroll 1
+                    for (uint32_t m = mask[cc]; m != 0u;) {
+                        int t[4];
+                        float gv[4], uv[4];
+                        take4(m, cc, t);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t col = lane_addr + static_cast<uint32_t>(max(t[i], 0));
+                            gv[i] = __uint_as_float(tmem_ld_32x32b_x1(col));
+                            uv[i] = __uint_as_float(tmem_ld_32x32b_x1(col + BNX));
+                        }
+                        tmem_ld_wait();
+                        if (whole) {
+                            mx4_store_h4(t, gv, uv, codes, I / 2, scale, zero_behind);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (t[i] >= 0) {
+                                    mine[t[i] * 128 + row] = gv[i];
+                                    mine[(BNX + t[i]) * 128 + row] = uv[i];
+                                }
                         }
                     }
-                }
             }
-            wb ^= 1;
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
@@ -337,6 +417,49 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 acc = 0;
                 acc_phase ^= 1u;
             }
+            if (whole)
+                continue;
+            const int64_t ut = (static_cast<int64_t>(g) * RT + tile) * KB;
+            const int64_t cf = dec_owner(ut, U, C), cl = dec_owner(ut + KB - 1, U, C);
+            dec_bar_sync();  // this CTA's partial is written
+            if (et == 0)
+                *last_flag = mx4_last_of(words + cf, call, static_cast<int>(cl - cf + 1));
+            dec_bar_sync();
+            if (*last_flag && inside) {
+                // their partials of two contributors in flight at a time
+#pragma unroll 1
+                for (int cc = 0; cc < BNX / 32; ++cc)
+#pragma unroll 1
+                    for (uint32_t m = mask[cc]; m != 0u;) {
+                        int t[4];
+                        float gv[4] = {0.f, 0.f, 0.f, 0.f}, uv[4] = {0.f, 0.f, 0.f, 0.f};
+                        take4(m, cc, t);
+                        for (int64_t c2 = cf; c2 <= cl; c2 += 2) {
+                            float a[2][4], b[2][4];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int64_t cs = min(c2 + k, cl);
+                                // slot 0: the tile a CTA's range begins in
+                                const float *p = ws + (cs * 2 + (dec_start(cs, U, C) >= ut ? 0 : 1)) * SLOT + row;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const bool on = t[i] >= 0 && c2 + k <= cl;
+                                    a[k][i] = on ? __ldcg(p + t[i] * 128) : 0.0f;
+                                    b[k][i] = on ? __ldcg(p + (BNX + t[i]) * 128) : 0.0f;
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    gv[i] += a[k][i];
+                                    uv[i] += b[k][i];
+                                }
+                        }
+                        mx4_store_h4(t, gv, uv, codes, I / 2, scale, zero_behind);
+                    }
+            }
+            dec_bar_sync();  // last_flag is rewritten by the next shared tile
         }
     }
 

@@ -18,7 +18,8 @@
 // them whatever N, K and the experts are.  A tile that several CTAs share is
 // summed through the workspace: each contributor writes its fp32 partial and
 // counts itself in, and the one that completes the count adds the partials in
-// the contributors' order, so the sum's order is fixed by the sizes alone.
+// the contributors' order, so the sum's order is fixed by the sizes alone.  The
+// kernel right before clears the counts.
 //
 // Scales.  A stage's scale tiles go from shared memory to TMEM columns that
 // belong to the stage (tcgen05.cp), so they are rewritten only after the
@@ -45,6 +46,7 @@ constexpr int kMx4MaxTokens = 128;   // of the streaming kernels
 constexpr int kMx4MaxSlots = 1024;   // tokens x choices of the experts layer
 constexpr int kMx4MaxExperts = 1024;
 constexpr int kMx4StreamThreads = 224;
+constexpr int kMx4MaxCtas = 160;  // of a streaming kernel: at least the SM count of every sm_100 part
 
 template <int BNX>
 struct Mx4StreamCfg {
@@ -64,42 +66,47 @@ struct Mx4StreamCfg {
 __host__ __device__ constexpr int mx4_stream_smem(int stage_bytes, int stages, bool moe)
 {
     return 1024 + stages * stage_bytes + (3 * stages + 5) * 8 + 24 +
-           (moe ? 2 * 512 + 2 * 16 + (kMx4MaxExperts / 32) * 4 + kMx4MaxExperts * 2 : 0);
+           (moe ? 2 * 512 + 2 * 16 + (kMx4MaxExperts / 32) * 4 + kMx4MaxExperts * 2 + kMx4MaxSlots * 2 : 0);
 }
 
 // The experts that any of the S choices names, ascending, into `list`; returns
-// their number.  Choices outside [0, E) name none.  All `threads` threads call
-// it (it ends with a barrier of the whole block).
+// their number.  Choices outside [0, E) name none.  The whole block calls it.
+// `chosen` [S] keeps the choices themselves, 0xFFFF for none.
 __device__ __forceinline__ int mx4_active_experts(const int *__restrict__ ids, int S, int E, uint32_t *mask,
-                                                  uint16_t *list, volatile int *count)
+                                                  uint16_t *list, uint16_t *chosen, volatile int *count)
 {
     for (int i = threadIdx.x; i < kMx4MaxExperts / 32; i += blockDim.x)
         mask[i] = 0u;
     __syncthreads();
     for (int i = threadIdx.x; i < S; i += blockDim.x) {
         const int e = __ldg(ids + i);
-        if (e >= 0 && e < E)
+        const bool here = e >= 0 && e < E;
+        chosen[i] = here ? static_cast<uint16_t>(e) : 0xFFFFu;
+        if (here)
             atomicOr(mask + (e >> 5), 1u << (e & 31));
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        uint32_t m = mask[lane];
-        int n = __popc(m), before = n;
+    // word w's first place in the list is the number of experts in the words
+    // before it: every warp scans the 32 words and lists the bits of some
+    const int lane = threadIdx.x & 31;
+    const uint32_t m = mask[lane];
+    int before = __popc(m);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
-            if (lane >= d)
-                before += o;
-        }
-        if (lane == 31)
-            *count = before;
-        before -= n;
-        while (m) {
-            list[before++] = static_cast<uint16_t>(lane * 32 + __ffs(m) - 1);
-            m &= m - 1;
-        }
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        if (lane >= d)
+            before += o;
     }
+    const int total = __shfl_sync(0xFFFFFFFFu, before, 31);
+    before -= __popc(m);
+    for (int w = threadIdx.x >> 5; w < (E + 31) / 32; w += blockDim.x >> 5) {
+        const uint32_t bits = __shfl_sync(0xFFFFFFFFu, m, w);
+        const int at = __shfl_sync(0xFFFFFFFFu, before, w);
+        if (bits & (1u << lane))
+            list[at + __popc(bits & ((1u << lane) - 1))] = static_cast<uint16_t>(w * 32 + lane);
+    }
+    if (threadIdx.x == 0)
+        *count = total;
     __syncthreads();
     return *count;
 }
@@ -128,6 +135,11 @@ __device__ __forceinline__ void mx4_stage_mma(uint32_t leader, uint32_t d, uint6
                          (k & 1) ? idesc_mx4(128, N, 2) : idesc_mx4(128, N, 0), ta + 4 * (k >> 1), tb + 4 * (k >> 1),
                          (first && k < NACC) ? 0u : 1u);
 }
+
+template <int V>
+struct Mx4Int {
+    static constexpr int value = V;
+};
 
 // Where a unit lies: tile, expert (its place in the list) and k block.  Made
 // once for the first unit of a range and stepped from there: dividing 64-bit
@@ -166,8 +178,7 @@ template <int BNX, int OUT, bool MOE>
 __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     mx4_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW,
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
-                      void *__restrict__ y, float *__restrict__ ws, int *__restrict__ cnt, int M, int N, int K,
-                      int ctas, int stages, int pre_wait, Mx4MoeArgs moe)
+                      void *__restrict__ y, float *__restrict__ ws, int *__restrict__ cnt, int M, int N, int K, int ctas, int stages, int pre_wait, Mx4MoeArgs moe)
 {
     using Cfg = Mx4StreamCfg<BNX>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -197,6 +208,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     uint32_t *wt_mask = reinterpret_cast<uint32_t *>(gb + misc_off + 24 + 1024);  // [2][4]
     uint32_t *e_mask = wt_mask + 8;
     uint16_t *e_list = reinterpret_cast<uint16_t *>(e_mask + kMx4MaxExperts / 32);
+    uint16_t *chosen = e_list + kMx4MaxExperts;
 
     if (threadIdx.x == 32) {
         for (int i = 0; i < stages; ++i) {
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int G = 1;
     if constexpr (MOE)
-        G = mx4_active_experts(moe.ids, M * moe.topk, moe.E, e_mask, e_list, n_groups);
+        G = mx4_active_experts(moe.ids, M * moe.topk, moe.E, e_mask, e_list, chosen, n_groups);
     if (pre_wait && !producer)
         asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -310,13 +322,13 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             // one accumulator: the k blocks of one tile and expert
             const int kb1 = min(KB, kb0 + left);
             left -= kb1 - kb0;
-            if (!bounded_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
+            if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, kErrWaitAccEmpty, abort_flag))
                 break;
             tc_fence_after_sync();
             const uint32_t d = tmem_base + static_cast<uint32_t>(acc * Cfg::NACC * BNX);
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!bounded_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
-                    !bounded_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                if (!warp_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
+                    !warp_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                     bool has = false;
                     if (et < M)
                         for (int k = 0; k < moe.topk; ++k)
-                            if (__ldg(moe.ids + et * moe.topk + k) == e) {
+                            if (chosen[et * moe.topk + k] == e) {
                                 w += __ldg(moe.weights + et * moe.topk + k);
                                 has = true;
                             }
@@ -493,30 +505,48 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             }
             dec_bar_sync();
             const int64_t cf = dec_owner(t * per_tile, U, C), cl = dec_owner((t + 1) * per_tile - 1, U, C);
-            if (et == 0) {
-                // release: this CTA's partial (ordered before it by the
-                // barrier) precedes the count; acquire: the others' partials
-                // precede the reads that follow
-                const int old = atom_add_acq_rel_gpu(cnt + t, 1);
-                *last_flag = old == static_cast<int>(cl - cf);
-            }
+            // release: this CTA's partial (ordered before it by the barrier)
+            // precedes the count; acquire: the others' partials precede the
+            // reads that follow.  A CTA is the first of at most one shared
+            // tile: its number is the count's.
+            if (et == 0)
+                *last_flag = atom_add_acq_rel_gpu(cnt + cf, 1) == static_cast<int>(cl - cf);
             dec_bar_sync();
             if (*last_flag) {
 #pragma unroll
                 for (int j = 0; j < BNX; ++j)
                     o[j] = 0.0f;
-                for (int64_t c2 = cf; c2 <= cl; ++c2) {
-                    const float4 *p = slot_of(c2) + row;
+                // CB contributors' loads in flight at a time (few tokens have few each)
+                auto reduce = [&](auto quads, auto contributors) {
+                    constexpr int Q = decltype(quads)::value, CB = decltype(contributors)::value;
+                    for (int64_t c2 = cf; c2 <= cl; c2 += CB) {
+                        float4 a[CB][Q];
 #pragma unroll
-                    for (int v = 0; v < BNX / 4; ++v)
-                        if (v < nv) {
-                            const float4 a = __ldcg(p + v * 128);
-                            o[4 * v] += a.x;
-                            o[4 * v + 1] += a.y;
-                            o[4 * v + 2] += a.z;
-                            o[4 * v + 3] += a.w;
+                        for (int i = 0; i < CB; ++i) {
+                            const float4 *p = slot_of(min(c2 + i, cl)) + row;
+#pragma unroll
+                            for (int v = 0; v < Q; ++v)
+                                a[i][v] = c2 + i <= cl && v < nv ? __ldcg(p + v * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
-                }
+#pragma unroll
+                        for (int i = 0; i < CB; ++i)
+#pragma unroll
+                            for (int v = 0; v < Q; ++v) {
+                                o[4 * v] += a[i][v].x;
+                                o[4 * v + 1] += a[i][v].y;
+                                o[4 * v + 2] += a[i][v].z;
+                                o[4 * v + 3] += a[i][v].w;
+                            }
+                    }
+                };
+                if (nv <= 1)
+                    reduce(Mx4Int<1>{}, Mx4Int<8>{});
+                else if (nv <= 4)
+                    reduce(Mx4Int<4>{}, Mx4Int<4>{});
+                else if constexpr (BNX <= 64)
+                    reduce(Mx4Int<BNX / 4>{}, Mx4Int<BNX == 32 ? 2 : 1>{});
+                else
+                    reduce(Mx4Int<BNX / 4>{}, Mx4Int<1>{});
                 if (n < N)
                     store(o, n);
             }

@@ -130,6 +130,14 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, unsi
     }
 }
 
+// bounded_wait of a whole converged warp, with one answer for all its lanes: what
+// follows stays uniform control flow, so that loop counters and addresses live in
+// uniform registers, where tcgen05 instructions take them.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned int code, volatile int *abort_flag)
+{
+    return __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity, code, abort_flag));
+}
+
 // ----------------------------------------------------------------------------
 // thread-block clusters: rank, distributed shared memory, cluster barriers
 // ----------------------------------------------------------------------------
@@ -205,6 +213,18 @@ __device__ __forceinline__ int atom_add_acq_rel_gpu(int *p, int v)
 {
     int old;
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
+// Compare and swap with release and acquire semantics at GPU scope; returns the old value.
+__device__ __forceinline__ unsigned long long atom_cas_acq_rel_gpu(unsigned long long *p, unsigned long long expected,
+                                                                   unsigned long long v)
+{
+    unsigned long long old;
+    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                 : "=l"(old)
+                 : "l"(p), "l"(expected), "l"(v)
+                 : "memory");
     return old;
 }
 
@@ -311,6 +331,14 @@ __device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap *map, int32
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap *map, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // ----------------------------------------------------------------------------
 // tcgen05: tensor memory, MMA, commit, loads
 // ----------------------------------------------------------------------------
@@ -378,6 +406,14 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
           "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+
+// One 32-bit column: thread i of the warp receives TMEM lane (lane_base + i).
+__device__ __forceinline__ uint32_t tmem_ld_32x32b_x1(uint32_t taddr)
+{
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    return r;
 }
 
 __device__ __forceinline__ void tmem_ld_wait()
