@@ -5,7 +5,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -135,23 +134,6 @@ bool make_tmap_scales(CUtensorMap *map, const uint8_t *scales, int64_t row_tiles
 using sq::kMx4MaxCtas;
 
 inline int mx4_bnx(int64_t M) { return M <= 32 ? 32 : (M <= 64 ? 64 : 128); }
-
-// A number for each call that no other call has, its lower 16 bits 0: the tile
-// counts carry it.  A random start and an odd step, so that what a workspace
-// happens to hold does not match.
-unsigned long long next_call_number()
-{
-    static std::atomic<unsigned long long> n{[] {
-        unsigned long long v = static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count());
-        v ^= reinterpret_cast<uintptr_t>(&v) << 20;
-        return v * 0x9E3779B97F4A7C15ull;
-    }()};
-    unsigned long long v;
-    do
-        v = n.fetch_add(0x9E3779B97F4A7C15ull) << 16;
-    while (v == 0);
-    return v;
-}
 
 constexpr size_t kMx4Words = kMx4MaxCtas * sizeof(unsigned long long);  // a tagged tile count for each CTA
 constexpr size_t kMx4Counts = kMx4MaxCtas * sizeof(int);                // a plain one
@@ -370,7 +352,6 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
     if (!ensure_smem_attr(up, Up::SMEM_BYTES, up_done) || !ensure_smem_attr(down, kMaxDynSmem, down_done))
         return SQ_ERR_CUDA;
     uint8_t *hq = c.ws, *hs = c.ws + c.L.hs;
-    unsigned long long *words = reinterpret_cast<unsigned long long *>(c.ws + c.L.words);
     int *cnt = reinterpret_cast<int *>(c.ws + c.L.cnt);
     float *slots = reinterpret_cast<float *>(c.ws + c.L.slots);
     const int64_t E = c.route.E, RI = (c.I + 127) / 128, RH = (c.H + 127) / 128;
@@ -383,7 +364,7 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
         return SQ_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(di.sms, kMx4MaxCtas));
     sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), Up::SMEM_BYTES, st, 0, 0,
-                                tg, tsg, tu, tsu, tx, tsx, td, tsd, hq, hs, slots, words, next_call_number(), cnt, static_cast<int>(c.T),
+                                tg, tsg, tu, tsu, tx, tsx, td, tsd, hq, hs, slots, c.route.words, cnt, static_cast<int>(c.T),
                                 static_cast<int>(c.H), static_cast<int>(c.I), kMx4Ahead, c.route);
     if (r != SQ_OK)
         return r;
@@ -580,7 +561,8 @@ sq_status sq_mx4_moe(const uint8_t *xq, const uint8_t *sx, const int32_t *ids, c
     const Mx4MoeWs L = mx4_moe_ws(T, topk, E, I);
     if (!ok_ptr(workspace) || ws_bytes < L.total)
         return SQ_ERR_INVALID_ARG;
-    const Mx4MoeCall c{xq, sx, wg, sg, wu, su, wd, sd, {ids, weights, static_cast<int>(topk), static_cast<int>(E)},
+    const Mx4MoeCall c{xq, sx, wg, sg, wu, su, wd, sd, {ids, weights, static_cast<int>(topk), static_cast<int>(E),
+                        reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(workspace) + L.words)},
                        T,  H,  I,  y,  static_cast<uint8_t *>(workspace), L};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return out_dt == SQ_BF16 ? launch_mx4_moe_bnx<OUT_BF16>(c, st) : launch_mx4_moe_bnx<OUT_F32>(c, st);

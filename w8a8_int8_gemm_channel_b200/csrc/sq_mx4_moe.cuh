@@ -58,28 +58,28 @@ struct Mx4UpCfg {
 };
 
 // Counts this CTA in at a shared tile's word and tells whether it is the last of
-// `total`.  The word's upper 48 bits are the call's number, which no other call
-// has, the lower 16 the count: whatever else a word holds counts as none, so a
-// workspace may hold anything, and the last one sets it back to 0, so that a
-// captured call may be replayed.  Release and acquire: the partials written
-// before (ordered by the caller's barrier) are visible to the last one.  (Nothing
-// runs before this kernel to clear a plain count; a plain count is a round trip
-// faster where contributors meet, so the second half uses one that this kernel
-// clears.)
-__device__ __forceinline__ bool mx4_last_of(unsigned long long *word, unsigned long long call, int total)
+// `total`.  Nothing runs before this kernel to clear the words, and the workspace
+// may hold anything.  So a word carries a tag in its upper 48 bits, and the lower
+// 16 count: the second half leaves every word at (tag, 0), and one add is enough
+// then.  A word without the tag (the workspace's first call) is replaced: whoever
+// finds it swaps in (tag, 1), or (tag, n + 1) where another one was faster; what
+// was added to it before that is lost with it.  Release and acquire: the partials
+// written before (ordered by the caller's barrier) are visible to the last one.
+__device__ __forceinline__ bool mx4_last_of(unsigned long long *word, int total)
 {
-    unsigned long long seen = 0, count;
-    for (;;) {
-        count = (seen >> 16) == (call >> 16) ? (seen & 0xFFFFu) + 1 : 1;
-        const unsigned long long old = atom_cas_acq_rel_gpu(word, seen, (call & ~0xFFFFull) | count);
-        if (old == seen)
-            break;
-        seen = old;  // every retry follows another contributor's success: at most `total` of them
+    unsigned long long seen = atom_add_acq_rel_gpu_u64(word, 1ull), count;
+    if ((seen & ~0xFFFFull) == kMx4Tag) {
+        count = (seen & 0xFFFFu) + 1;
+    } else {
+        for (;;) {  // a failed swap means that another contributor came between: at most 2 * total of them
+            count = (seen & ~0xFFFFull) == kMx4Tag ? (seen & 0xFFFFu) + 1 : 1;
+            const unsigned long long old = atom_cas_acq_rel_gpu(word, seen, kMx4Tag | count);
+            if (old == seen)
+                break;
+            seen = old;
+        }
     }
-    if (count != static_cast<unsigned long long>(total))
-        return false;
-    *reinterpret_cast<volatile unsigned long long *>(word) = 0;
-    return true;
+    return count == static_cast<unsigned long long>(total);
 }
 
 // The E2M1 code of one scaled value (bits 0-3).
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
                       const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmSD,
                       uint8_t *__restrict__ hq, uint8_t *__restrict__ hs, float *__restrict__ ws,
-                      unsigned long long *__restrict__ words, unsigned long long call, int *__restrict__ cnt, int M, int H, int I,
+                      unsigned long long *__restrict__ words, int *__restrict__ cnt, int M, int H, int I,
                       int ahead, Mx4MoeArgs moe)
 {
     using Cfg = Mx4UpCfg<BNX>;
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             const int64_t cf = dec_owner(ut, U, C), cl = dec_owner(ut + KB - 1, U, C);
             dec_bar_sync();  // this CTA's partial is written
             if (et == 0)
-                *last_flag = mx4_last_of(words + cf, call, static_cast<int>(cl - cf + 1));
+                *last_flag = mx4_last_of(words + cf, static_cast<int>(cl - cf + 1));
             dec_bar_sync();
             if (*last_flag && inside) {
                 // their partials of two contributors in flight at a time

@@ -46,6 +46,7 @@ constexpr int kMx4MaxTokens = 128;   // of the streaming kernels
 constexpr int kMx4MaxSlots = 1024;   // tokens x choices of the experts layer
 constexpr int kMx4MaxExperts = 1024;
 constexpr int kMx4StreamThreads = 224;
+constexpr unsigned long long kMx4Tag = 0x9E3779B97F4Aull << 16;  // of a tile word (see mx4_last_of)
 constexpr int kMx4MaxCtas = 160;  // of a streaming kernel: at least the SM count of every sm_100 part
 
 template <int BNX>
@@ -172,6 +173,7 @@ struct Mx4MoeArgs {
     const int *ids;        // [T, topk]
     const float *weights;  // [T, topk]
     int topk, E;
+    unsigned long long *words;  // the first half's tile words, set back here for the next call
 };
 
 template <int BNX, int OUT, bool MOE>
@@ -250,6 +252,10 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
         G = mx4_active_experts(moe.ids, M * moe.topk, moe.E, e_mask, e_list, chosen, n_groups);
     if (pre_wait && !producer)
         asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (MOE) {
+        if (threadIdx.x == 64 && blockIdx.x < kMx4MaxCtas)
+            moe.words[blockIdx.x] = kMx4Tag;
+    }
 
     const int T = (N + 127) / 128;
     const int KB = (K + kMx4KB - 1) / kMx4KB;

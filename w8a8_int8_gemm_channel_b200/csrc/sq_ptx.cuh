@@ -216,6 +216,13 @@ __device__ __forceinline__ int atom_add_acq_rel_gpu(int *p, int v)
     return old;
 }
 
+__device__ __forceinline__ unsigned long long atom_add_acq_rel_gpu_u64(unsigned long long *p, unsigned long long v)
+{
+    unsigned long long old;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
+    return old;
+}
+
 // Compare and swap with release and acquire semantics at GPU scope; returns the old value.
 __device__ __forceinline__ unsigned long long atom_cas_acq_rel_gpu(unsigned long long *p, unsigned long long expected,
                                                                    unsigned long long v)
