@@ -360,6 +360,11 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                     tok_mask[wb * 4 + (et >> 5)] = m;
                 dec_bar_sync();
             }
+            // a shared tile's contributors (worked out while the tile streams);
+            // only the first one's range may begin in an earlier tile
+            const int64_t ut = (static_cast<int64_t>(g) * RT + tile) * KB;
+            const int64_t cf = whole ? 0 : dec_owner(ut, U, C), cl = whole ? 0 : dec_owner(ut + KB - 1, U, C);
+            const int cf_slot = !whole && dec_start(cf, U, C) < ut;
             const uint32_t *mask = tok_mask + wb * 4;
             wb ^= 1;
             // as in mx4_stream_kernel, a wait that gives up lets the warps go on
@@ -419,8 +424,6 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             }
             if (whole)
                 continue;
-            const int64_t ut = (static_cast<int64_t>(g) * RT + tile) * KB;
-            const int64_t cf = dec_owner(ut, U, C), cl = dec_owner(ut + KB - 1, U, C);
             dec_bar_sync();  // this CTA's partial is written
             if (et == 0)
                 *last_flag = mx4_last_of(words + cf, static_cast<int>(cl - cf + 1));
@@ -439,8 +442,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const int64_t cs = min(c2 + k, cl);
-                                // slot 0: the tile a CTA's range begins in
-                                const float *p = ws + (cs * 2 + (dec_start(cs, U, C) >= ut ? 0 : 1)) * SLOT + row;
+                                const float *p = ws + (cs * 2 + (cs == cf ? cf_slot : 0)) * SLOT + row;
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     const bool on = t[i] >= 0 && c2 + k <= cl;

@@ -420,6 +420,10 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             const int64_t seg_end = min(u1, (t + 1) * per_tile);
             const bool whole = seg_begin == t * per_tile && seg_end == (t + 1) * per_tile;
             const int64_t n = t * 128 + row;
+            // a shared tile's contributors (worked out while the tile streams)
+            const int64_t cf = whole ? 0 : dec_owner(t * per_tile, U, C);
+            const int64_t cl = whole ? 0 : dec_owner((t + 1) * per_tile - 1, U, C);
+            const int cf_slot = !whole && dec_start(cf, U, C) < t * per_tile;
             float o[BNX];
 #pragma unroll
             for (int j = 0; j < BNX; ++j)
@@ -498,9 +502,9 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             }
             // this range's part of a shared tile: 4 tokens x 128 rows at a time
             const int nv = (M + 3) >> 2;
+            // only the first contributor's range may begin in an earlier tile
             auto slot_of = [&](int64_t c2) {
-                return reinterpret_cast<float4 *>(ws) +
-                       (c2 * 2 + (dec_start(c2, U, C) / per_tile == t ? 0 : 1)) * (BNX / 4 * 128);
+                return reinterpret_cast<float4 *>(ws) + (c2 * 2 + (c2 == cf ? cf_slot : 0)) * (BNX / 4 * 128);
             };
             {
                 float4 *mine = reinterpret_cast<float4 *>(ws) + (c * 2 + (t == first_tile ? 0 : 1)) * (BNX / 4 * 128);
@@ -510,7 +514,6 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                         mine[v * 128 + row] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
             }
             dec_bar_sync();
-            const int64_t cf = dec_owner(t * per_tile, U, C), cl = dec_owner((t + 1) * per_tile - 1, U, C);
             // release: this CTA's partial (ordered before it by the barrier)
             // precedes the count; acquire: the others' partials precede the
             // reads that follow.  A CTA is the first of at most one shared
