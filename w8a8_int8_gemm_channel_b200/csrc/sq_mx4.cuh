@@ -39,6 +39,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return d;
 }
 
+// max(a, |b|, |c|), NaN if any is
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // 8 consecutive values of dtype T as fp32
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, float (&v)[8]);
@@ -61,6 +69,44 @@ template <>
 __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8])
 {
     bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p)), v);
+}
+
+template <typename T>
+struct Raw8;  // 8 values as loaded
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+};
+
+__device__ __forceinline__ void raw_load(Raw8<__nv_bfloat16> &r, const __nv_bfloat16 *p)
+{
+    r.a = *reinterpret_cast<const uint4 *>(p);
+}
+__device__ __forceinline__ void raw_load(Raw8<float> &r, const float *p)
+{
+    r.a = reinterpret_cast<const float4 *>(p)[0];
+    r.b = reinterpret_cast<const float4 *>(p)[1];
+}
+// through the read-only path
+__device__ __forceinline__ void raw_load_nc(Raw8<__nv_bfloat16> &r, const __nv_bfloat16 *p)
+{
+    r.a = __ldg(reinterpret_cast<const uint4 *>(p));
+}
+__device__ __forceinline__ void raw_load_nc(Raw8<float> &r, const float *p)
+{
+    r.a = __ldg(reinterpret_cast<const float4 *>(p));
+    r.b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+}
+__device__ __forceinline__ void raw_zero(Raw8<__nv_bfloat16> &r) { r.a = make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void raw_zero(Raw8<float> &r) { r.a = r.b = make_float4(0, 0, 0, 0); }
+__device__ __forceinline__ void raw_values(const Raw8<__nv_bfloat16> &r, float (&v)[8]) { bf16x8_to_f32(r.a, v); }
+__device__ __forceinline__ void raw_values(const Raw8<float> &r, float (&v)[8])
+{
+    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w, v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
 }
 
 // v[i] * f[i] and v[i] * f, two at a time (packed fp32, rounded like the scalar)
@@ -132,8 +178,8 @@ __device__ __forceinline__ void mx4_store_chunk(const float (&v)[8], bool in_k, 
 {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        top = max_nan(top, fabsf(v[i]));
+    for (int i = 0; i < 8; i += 2)
+        top = max3_abs(top, v[i], v[i + 1]);
     top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     uint32_t byte = mx4_scale_byte(top);
@@ -157,27 +203,30 @@ __device__ __forceinline__ void mx4_zero_pad(uint8_t *scales, int64_t rows, int6
         *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(rows + i / KT, i % KT, KT)) = 0u;
 }
 
-// Quantiser.  A thread owns 8 columns (its factors stay in registers) and
-// walks down the rows of its band, U rows in flight; 16 neighbouring threads
-// make one word of scale bytes.  A CTA covers TX * 8 columns, TX a multiple of
-// 16, and 256 / TX rows at a time.  Memory-bound: 2 or 4 bytes in and 17/32 out
-// a value; the smoothing divides by multiplying with RN(1 / s), one division a
+// Quantiser.  A thread owns 8 columns (its factors stay in registers) and walks
+// down the rows of its band, U rows in flight; 16 neighbouring threads make one
+// word of scale bytes.  A CTA covers TX * 8 columns, TX a multiple of 16, and 256
+// / TX rows at a time.  Memory-bound for fp32 (4096 x 8192 at 5.3 TB/s); with
+// bf16's 2.5 bytes a value the instructions count too, so the maximum takes three
+// operands an instruction and the products are packed.  (16 columns a thread
+// halve the shuffles but spread each load over twice the lines: 28672 x 4096 in
+// 94 us.)  The smoothing divides by multiplying with RN(1 / s), one division a
 // column and band instead of one a value.
 // `zero`: tile counts of the product after it, cleared on the side.
 template <typename T, int OP>
-__global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restrict__ x, int64_t rows, int64_t K,
+__global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restrict__ x, int rows, int K,
                                                                 const float *__restrict__ s,
                                                                 uint8_t *__restrict__ codes,
-                                                                uint8_t *__restrict__ scales, int log2tx,
-                                                                int64_t band, int *__restrict__ zero, int nzero)
+                                                                uint8_t *__restrict__ scales, int log2tx, int band,
+                                                                int *__restrict__ zero, int nzero)
 {
     pdl_prologue();
     constexpr int U = 4;
     const int tx = threadIdx.x & ((1 << log2tx) - 1), ty = threadIdx.x >> log2tx;
     const int TY = kMx4Threads >> log2tx;
-    const int64_t KT = (K + 127) >> 7;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x) << log2tx) + tx;  // chunk of 8 columns
-    const int64_t kt = c >> 4;
+    const int KT = (K + 127) >> 7;
+    const int c = (static_cast<int>(blockIdx.x) << log2tx) + tx;  // chunk of 8 columns
+    const int kt = c >> 4;
     const bool in_k = c * 8 < K;
     const bool word_lane = (threadIdx.x & 15) == 0 && kt < KT;
     float f[8];
@@ -188,32 +237,37 @@ __global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restr
         for (int i = 0; i < 8; ++i)
             f[i] = !in_k ? 1.0f : (OP == MX4_OVER ? __frcp_rn(f[i]) : f[i]);
     }
-    const int64_t r0 = blockIdx.y * band, r1 = min(rows, r0 + band);
-    // every lane of a warp takes the same trips (rows behind the end are
-    // clamped for the loads and not stored), so the shuffles are whole
-    for (int64_t rb = r0; rb < r1; rb += static_cast<int64_t>(TY) * U) {
-        float v[U][8];
+    const int r0 = static_cast<int>(blockIdx.y) * band, r1 = min(rows, r0 + band);
+    const T *px = x + (static_cast<int64_t>(r0) + ty) * K + c * 8;
+    uint8_t *pq = codes + (static_cast<int64_t>(r0) + ty) * (K / 2) + c * 4;
+    uint8_t *ps = scales + static_cast<int64_t>(kt) * kMx4TileBytes;
+    const int64_t xstep = static_cast<int64_t>(TY) * K, row_tile = static_cast<int64_t>(KT) * kMx4TileBytes;
+    // every lane of a warp takes the same trips (rows behind the end are neither
+    // loaded nor stored), so the shuffles are whole
+    for (int rb = r0; rb < r1; rb += TY * U) {
+        Raw8<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t r = rb + ty + static_cast<int64_t>(u) * TY;
-            if (in_k && r < r1) {
-                load8<T>(x + r * K + c * 8, v[u]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[u][i] = 0.0f;
-            }
+            if (in_k && rb + ty + u * TY < r1)
+                raw_load_nc(raw[u], px + u * xstep);
+            else
+                raw_zero(raw[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t r = rb + ty + static_cast<int64_t>(u) * TY;
-            if constexpr (OP != MX4_PLAIN)
-                mul8(v[u], f);
+            const int r = rb + ty + u * TY;
             const bool live = r < r1;
-            mx4_store_chunk(v[u], in_k && live, reinterpret_cast<uint32_t *>(codes + r * (K / 2) + c * 4),
-                            word_lane && live ? reinterpret_cast<uint32_t *>(scales + mx4_scale_word(r, kt, KT))
+            float v[8];
+            raw_values(raw[u], v);
+            if constexpr (OP != MX4_PLAIN)
+                mul8(v, f);
+            mx4_store_chunk(v, in_k && live, reinterpret_cast<uint32_t *>(pq + u * (xstep / 2)),
+                            word_lane && live ? reinterpret_cast<uint32_t *>(ps + (r >> 7) * row_tile + (r & 31) * 16 +
+                                                                            ((r >> 5) & 3) * 4)
                                               : nullptr);
         }
+        px += xstep * U;
+        pq += xstep / 2 * U;
     }
     const int64_t nt = static_cast<int64_t>(gridDim.x) * gridDim.y * kMx4Threads;
     const int64_t me = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kMx4Threads + threadIdx.x;
@@ -238,54 +292,60 @@ __device__ __forceinline__ __half2 e2m1x2_to_half2(uint32_t byte)
 // and in bf16 (subnormal ones included).
 template <typename T>
 __global__ void __launch_bounds__(kMx4Threads) mx4_dequant_kernel(const uint8_t *__restrict__ codes,
-                                                                  const uint8_t *__restrict__ scales, int64_t rows,
-                                                                  int64_t K, T *__restrict__ out, int log2tx,
-                                                                  int64_t band)
+                                                                  const uint8_t *__restrict__ scales, int rows, int K,
+                                                                  T *__restrict__ out, int log2tx, int band)
 {
     pdl_prologue();
     constexpr int U = 4;
     const int tx = threadIdx.x & ((1 << log2tx) - 1), ty = threadIdx.x >> log2tx;
     const int TY = kMx4Threads >> log2tx;
-    const int64_t KT = (K + 127) >> 7;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x) << log2tx) + tx;
+    const int KT = (K + 127) >> 7;
+    const int c = (static_cast<int>(blockIdx.x) << log2tx) + tx;
     if (c * 8 >= K)
         return;
-    const int64_t r0 = blockIdx.y * band, r1 = min(rows, r0 + band);
-    for (int64_t rb = r0 + ty; rb < r1; rb += static_cast<int64_t>(TY) * U) {
+    const int r0 = static_cast<int>(blockIdx.y) * band, r1 = min(rows, r0 + band);
+    const uint8_t *pq = codes + (static_cast<int64_t>(r0) + ty) * (K / 2) + c * 4;
+    const uint8_t *ps = scales + static_cast<int64_t>(c >> 4) * kMx4TileBytes + ((c >> 2) & 3);
+    T *po = out + (static_cast<int64_t>(r0) + ty) * K + c * 8;
+    const int64_t step = static_cast<int64_t>(TY) * K, row_tile = static_cast<int64_t>(KT) * kMx4TileBytes;
+    for (int rb = r0 + ty; rb < r1; rb += TY * U) {
         uint32_t q[U], b[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t r = min(rb + static_cast<int64_t>(u) * TY, r1 - 1);
-            q[u] = __ldg(reinterpret_cast<const uint32_t *>(codes + r * (K / 2) + c * 4));
-            b[u] = __ldg(scales + mx4_scale_word(r, c >> 4, KT) + ((c >> 2) & 3));
+            const int r = rb + u * TY;
+            if (r < r1) {
+                q[u] = __ldg(reinterpret_cast<const uint32_t *>(pq + u * (step / 2)));
+                b[u] = __ldg(ps + (r >> 7) * row_tile + (r & 31) * 16 + ((r >> 5) & 3) * 4);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t r = rb + static_cast<int64_t>(u) * TY;
-            if (r >= r1)
+            if (rb + u * TY >= r1)
                 break;
-            const float sc = mx4_scale(b[u]);
             float v[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 p = __half22float2(e2m1x2_to_half2((q[u] >> (8 * i)) & 0xFFu));
-                v[2 * i] = __fmul_rn(p.x, sc);
-                v[2 * i + 1] = __fmul_rn(p.y, sc);
+                v[2 * i] = p.x;
+                v[2 * i + 1] = p.y;
             }
-            T *dst = out + r * K + c * 8;
+            mul8(v, mx4_scale(b[u]));
+            T *dst = po + u * step;
             if constexpr (sizeof(T) == 4) {
                 reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
                 reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
             } else {
-                uint32_t w[4];
+                uint32_t o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                    const __nv_bfloat162 x2 = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    o[i] = *reinterpret_cast<const uint32_t *>(&x2);
                 }
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
+        pq += step / 2 * U;
+        po += step * U;
     }
 }
 

@@ -52,9 +52,8 @@ inline size_t scale_bytes(int64_t rows, int64_t K)
 // The CTA covers 2^log2tx chunks of 8 columns; the row bands fill every SM
 // about eight times over.
 struct Mx4Walk {
-    int log2tx;
+    int log2tx, band;
     unsigned gx, gy;
-    int64_t band;
 };
 
 inline Mx4Walk mx4_walk(int64_t rows, int64_t K, int64_t sms)
@@ -65,11 +64,12 @@ inline Mx4Walk mx4_walk(int64_t rows, int64_t K, int64_t sms)
     const int64_t TX = int64_t{1} << w.log2tx, step = sq::kMx4Threads / TX * 4;
     const int64_t gx = (chunks + TX - 1) / TX;
     const int64_t want = std::max<int64_t>(1, sms * 8 / gx);
-    w.band = std::max<int64_t>(step, ((rows + want - 1) / want + step - 1) / step * step);
-    while ((rows + w.band - 1) / w.band > 65535)
-        w.band *= 2;
+    int64_t band = std::max<int64_t>(step, ((rows + want - 1) / want + step - 1) / step * step);
+    while ((rows + band - 1) / band > 65535)
+        band *= 2;
+    w.band = static_cast<int>(band);
     w.gx = static_cast<unsigned>(gx);
-    w.gy = static_cast<unsigned>((rows + w.band - 1) / w.band);
+    w.gy = static_cast<unsigned>((rows + band - 1) / band);
     return w;
 }
 
@@ -84,7 +84,8 @@ sq_status launch_mx4_quant(const T *x, int64_t rows, int64_t K, const float *s, 
     auto kernel = s == nullptr ? sq::mx4_quant_kernel<T, sq::MX4_PLAIN>
                                : (op == sq::MX4_TIMES ? sq::mx4_quant_kernel<T, sq::MX4_TIMES>
                                                       : sq::mx4_quant_kernel<T, sq::MX4_OVER>);
-    return launch_kernel(kernel, dim3(w.gx, w.gy), dim3(sq::kMx4Threads), 0, st, 0, 0, x, rows, K, s, q, sc, w.log2tx,
+    return launch_kernel(kernel, dim3(w.gx, w.gy), dim3(sq::kMx4Threads), 0, st, 0, 0, x, static_cast<int>(rows),
+                         static_cast<int>(K), s, q, sc, w.log2tx,
                          w.band, zero, nzero);
 }
 
@@ -480,9 +481,9 @@ sq_status sq_mx4_dequant(const uint8_t *q, const uint8_t *sc, int64_t rows, int6
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (out_dt == SQ_BF16)
         return launch_kernel(sq::mx4_dequant_kernel<__nv_bfloat16>, dim3(w.gx, w.gy), dim3(sq::kMx4Threads), 0, st, 0, 0,
-                             q, sc, rows, K, static_cast<__nv_bfloat16 *>(out), w.log2tx, w.band);
+                             q, sc, static_cast<int>(rows), static_cast<int>(K), static_cast<__nv_bfloat16 *>(out), w.log2tx, w.band);
     return launch_kernel(sq::mx4_dequant_kernel<float>, dim3(w.gx, w.gy), dim3(sq::kMx4Threads), 0, st, 0, 0, q, sc,
-                         rows, K, static_cast<float *>(out), w.log2tx, w.band);
+                         static_cast<int>(rows), static_cast<int>(K), static_cast<float *>(out), w.log2tx, w.band);
 }
 
 size_t sq_mx4_gemm_workspace_size(int64_t M, int64_t N, int64_t K)

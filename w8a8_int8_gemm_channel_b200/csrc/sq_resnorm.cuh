@@ -27,35 +27,8 @@
 
 namespace sq {
 
-template <typename T>
-struct ResRaw;  // 8 values as loaded
-template <>
-struct ResRaw<__nv_bfloat16> {
-    uint4 a;
-};
-template <>
-struct ResRaw<float> {
-    float4 a, b;
-};
-
-__device__ __forceinline__ void res_load(ResRaw<__nv_bfloat16> &r, const __nv_bfloat16 *p)
-{
-    r.a = *reinterpret_cast<const uint4 *>(p);
-}
-__device__ __forceinline__ void res_load(ResRaw<float> &r, const float *p)
-{
-    r.a = reinterpret_cast<const float4 *>(p)[0];
-    r.b = reinterpret_cast<const float4 *>(p)[1];
-}
-__device__ __forceinline__ void res_zero(ResRaw<__nv_bfloat16> &r) { r.a = make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void res_zero(ResRaw<float> &r) { r.a = r.b = make_float4(0, 0, 0, 0); }
-__device__ __forceinline__ void res_values(const ResRaw<__nv_bfloat16> &r, float (&v)[8]) { bf16x8_to_f32(r.a, v); }
-__device__ __forceinline__ void res_values(const ResRaw<float> &r, float (&v)[8])
-{
-    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w, v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
-}
 // rounds to T and stores; `r` keeps what was stored
-__device__ __forceinline__ void res_store(ResRaw<__nv_bfloat16> &r, __nv_bfloat16 *p, const float (&v)[8])
+__device__ __forceinline__ void res_store(Raw8<__nv_bfloat16> &r, __nv_bfloat16 *p, const float (&v)[8])
 {
     uint32_t w[4];
 #pragma unroll
@@ -66,7 +39,7 @@ __device__ __forceinline__ void res_store(ResRaw<__nv_bfloat16> &r, __nv_bfloat1
     r.a = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4 *>(p) = r.a;
 }
-__device__ __forceinline__ void res_store(ResRaw<float> &r, float *p, const float (&v)[8])
+__device__ __forceinline__ void res_store(Raw8<float> &r, float *p, const float (&v)[8])
 {
     r.a = make_float4(v[0], v[1], v[2], v[3]);
     r.b = make_float4(v[4], v[5], v[6], v[7]);
@@ -182,17 +155,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) res_norm_kernel(const ResArgs
             load8<float>(global + c, f);
         }
     };
-    ResRaw<T> bv[CH], rv[CH], bn[AHEAD ? CH : 1], rn[AHEAD ? CH : 1];
-    auto fetch = [&](int64_t m, ResRaw<T> *x, ResRaw<T> *y) {
+    Raw8<T> bv[CH], rv[CH], bn[AHEAD ? CH : 1], rn[AHEAD ? CH : 1];
+    auto fetch = [&](int64_t m, Raw8<T> *x, Raw8<T> *y) {
         const T *pb = b + m * K, *pr = r + m * K;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             if (col[i] < K && m < p.M) {
-                res_load(x[i], pb + col[i]);
-                res_load(y[i], pr + col[i]);
+                raw_load(x[i], pb + col[i]);
+                raw_load(y[i], pr + col[i]);
             } else {
-                res_zero(x[i]);
-                res_zero(y[i]);
+                raw_zero(x[i]);
+                raw_zero(y[i]);
             }
         }
     };
@@ -216,7 +189,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) res_norm_kernel(const ResArgs
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 float v[8];
-                res_values(bv[i], v);
+                raw_values(bv[i], v);
                 s += res_squares(v);
             }
             rb = res_rinv<THREADS>(s, inv_k, p.eps, sums[parity][0]);
@@ -229,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) res_norm_kernel(const ResArgs
             if (col[i] >= K)
                 continue;
             float u[8], f[8], o[8];
-            res_values(bv[i], u);
+            raw_values(bv[i], u);
             if (post) {
                 factor(p.gamma, 0, col[i], f);
                 mul8(u, rb);
@@ -239,19 +212,19 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) res_norm_kernel(const ResArgs
                 load8<T>(gr + col[i], f);
                 mul8(u, f);
             }
-            res_values(rv[i], o);
+            raw_values(rv[i], o);
             // scalar: a packed product and sum would be fused into one rounding
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 o[j] = __fadd_rn(o[j], __fmul_rn(u[j], p.c));
             res_store(rv[i], po + col[i], o);
-            res_values(rv[i], o);
+            raw_values(rv[i], o);
             s += res_squares(o);
         }
         const float ra = res_rinv<THREADS>(s, inv_k, p.eps, sums[parity][1]);
         auto scaled = [&](int i, float (&a)[8]) {
             float f[8];
-            res_values(rv[i], a);
+            raw_values(rv[i], a);
             factor(p.g, K, col[i], f);
             mul8(a, ra);
             mul8(a, f);
