@@ -367,12 +367,34 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+_codes_of = {}  # torch dtype -> code of the mx4 calls, and what else of torch they use (filled once it is imported)
+
+
+def _torch_parts():
+    """(uint8, float32, current device's number, current stream's raw handle of a device)."""
+    parts = _codes_of.get("parts")
+    if parts is None:
+        torch = _torch()
+        _codes_of[torch.float32], _codes_of[torch.bfloat16] = SQ_F32, SQ_BF16
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        parts = _codes_of["parts"] = (torch.uint8, torch.float32, device, raw)
+    return parts
+
+
+def _code(t) -> int:
+    c = _codes_of.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {t.dtype}; expected float32 or bfloat16")
+    return c
+
+
 def _mx4_ptrs(rows: int, K: int, q, sc):
     """Device pointers of codes and scales, their sizes checked against [rows, K]."""
-    u8 = _torch().uint8
+    u8 = _torch_parts()[0]
     if q.dtype is not u8 or q.shape != (rows, K // 2):
         raise ValueError(f"codes: uint8 of shape {(rows, K // 2)}")
-    if sc.dtype is not u8 or sc.numel() < -(-rows // 128) * -(-K // 128) * 512:
+    if sc.dtype is not u8 or sc.numel() < ((rows + 127) >> 7) * ((K + 127) >> 7) * 512:
         raise ValueError(f"scales: uint8 of sq_mx4_scale_size({rows}, {K}) bytes")
     return q.data_ptr(), sc.data_ptr()
 
@@ -380,7 +402,7 @@ def _mx4_ptrs(rows: int, K: int, q, sc):
 def _mx4_factors(s, K: int):
     if s is None:
         return None
-    if s.dtype is not _torch().float32 or s.numel() != K:
+    if s.dtype is not _torch_parts()[1] or s.numel() != K:
         raise ValueError(f"s: float32 of {K} values")
     return s.data_ptr()
 
@@ -392,7 +414,7 @@ def _ws_args(ws):
 def _call(name, stream, tensors, make_args):
     """Calls an entry point with the tensors' device current: every tensor on one device and contiguous (None: left
     out).  make_args() gives the arguments before the stream."""
-    torch = _torch()
+    _, _, device, raw_stream = _torch_parts()
     d = tensors[0].get_device()
     for t in tensors:
         if t is not None and (t.get_device() != d or d < 0 or not t.is_contiguous()):
@@ -400,11 +422,11 @@ def _call(name, stream, tensors, make_args):
                 raise ValueError("libsq takes device tensors")
             raise ValueError("libsq takes contiguous tensors" if t.get_device() == d else f"tensors on devices {d} and {t.get_device()}")
     f = getattr(_lib or lib(), name)
-    if d == torch.cuda.current_device():
-        st = f(*make_args(), _stream(stream))
+    if d == device():
+        st = f(*make_args(), raw_stream(d) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(d):
-            st = f(*make_args(), _stream(stream))
+        with _torch().cuda.device(d):
+            st = f(*make_args(), raw_stream(d) if stream is None else _stream(stream))
     if st != SQ_OK:
         raise SQError(name, st, status_string(st))
 
@@ -417,20 +439,20 @@ def sq_mx4_scale_size(rows: int, K: int) -> int:
 def sq_mx4_quant_act(x, s, xq, sx, stream=None):
     M, K = x.shape
     _call("sq_mx4_quant_act", stream, (x, s, xq, sx),
-          lambda: (x.data_ptr(), _dtype_code(x), M, K, _mx4_factors(s, K), *_mx4_ptrs(M, K, xq, sx)))
+          lambda: (x.data_ptr(), _code(x), M, K, _mx4_factors(s, K), *_mx4_ptrs(M, K, xq, sx)))
 
 
 def sq_mx4_quant_weight(w, s, wq, sw, stream=None):
     N, K = w.shape
     _call("sq_mx4_quant_weight", stream, (w, s, wq, sw),
-          lambda: (w.data_ptr(), _dtype_code(w), N, K, _mx4_factors(s, K), *_mx4_ptrs(N, K, wq, sw)))
+          lambda: (w.data_ptr(), _code(w), N, K, _mx4_factors(s, K), *_mx4_ptrs(N, K, wq, sw)))
 
 
 def sq_mx4_dequant(q, sc, out, stream=None):
     """out [rows, K] (float32 or bfloat16): the values the codes stand for."""
     rows, K = out.shape
     _call("sq_mx4_dequant", stream, (out, q, sc),
-          lambda: (*_mx4_ptrs(rows, K, q, sc), rows, K, out.data_ptr(), _dtype_code(out)))
+          lambda: (*_mx4_ptrs(rows, K, q, sc), rows, K, out.data_ptr(), _code(out)))
 
 
 def sq_mx4_gemm_workspace_size(M: int, N: int, K: int) -> int:
@@ -444,7 +466,7 @@ def sq_mx4_gemm(xq, sx, wq, sw, y, workspace=None, stream=None):
     if workspace is None:
         workspace = _torch().empty(sq_mx4_gemm_workspace_size(M, N, K), dtype=_torch().uint8, device=y.device)
     _call("sq_mx4_gemm", stream, (y, xq, sx, wq, sw, workspace),
-          lambda: (*_mx4_ptrs(M, K, xq, sx), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(), _dtype_code(y),
+          lambda: (*_mx4_ptrs(M, K, xq, sx), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(), _code(y),
                    *_ws_args(workspace)))
 
 
@@ -461,8 +483,8 @@ def sq_mx4_linear(x, s, wq, sw, y, workspace=None, stream=None):
     if workspace is None:
         workspace = _torch().empty(sq_mx4_linear_workspace_size(M, N, K), dtype=_torch().uint8, device=x.device)
     _call("sq_mx4_linear", stream, (x, s, wq, sw, y, workspace),
-          lambda: (x.data_ptr(), _dtype_code(x), _mx4_factors(s, K), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(),
-                   _dtype_code(y), *_ws_args(workspace)))
+          lambda: (x.data_ptr(), _code(x), _mx4_factors(s, K), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(),
+                   _code(y), *_ws_args(workspace)))
 
 
 def sq_mx4_moe_workspace_size(T: int, topk: int, E: int, H: int, I: int) -> int:
@@ -491,7 +513,7 @@ def sq_mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, y, workspace=None, 
     _call("sq_mx4_moe", stream, (y, xq, sx, ids, weights, wg, sg, wu, su, wd, sd, workspace),
           lambda: (*_mx4_ptrs(T, H, xq, sx), ids.data_ptr(), weights.data_ptr(), T, topk, E, H, I, wg.data_ptr(),
                    sg.data_ptr(), wu.data_ptr(), su.data_ptr(), wd.data_ptr(), sd.data_ptr(), y.data_ptr(),
-                   _dtype_code(y), *_ws_args(workspace)))
+                   _code(y), *_ws_args(workspace)))
 
 
 def _residual_norm(name, b, gamma, gate, gate_tokens, c, r, r_out, g, eps, q, sx, stream):
@@ -502,7 +524,7 @@ def _residual_norm(name, b, gamma, gate, gate_tokens, c, r, r_out, g, eps, q, sx
                              gate.numel() < -(-M // gate_tokens) * K):
         raise ValueError("gate: b's dtype, a row for every gate_tokens tokens")
     _call(name, stream, (b, gamma, gate, r, r_out, g, q, sx),
-          lambda: (b.data_ptr(), _dtype_code(b), M, K, _mx4_factors(gamma, K), None if gate is None else gate.data_ptr(),
+          lambda: (b.data_ptr(), _code(b), M, K, _mx4_factors(gamma, K), None if gate is None else gate.data_ptr(),
                    int(gate_tokens), float(c), r.data_ptr(), r_out.data_ptr(), _mx4_factors(g, K), float(eps),
                    q.data_ptr(), sx.data_ptr()))
 
