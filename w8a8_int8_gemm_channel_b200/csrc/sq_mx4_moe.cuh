@@ -23,7 +23,9 @@
 // to hide the loaded memory's latency; two experts of 4096 x 14336 took 38 us.)
 //
 // A tile that several CTAs share is summed through the workspace; the last of
-// them (mx4_last_of) adds the partials in the contributors'
+// them (mx4_last_of, or before that a look at the count while its part still
+// streams, which spares it writing and counting its own partial: with fewer k
+// blocks a tile than units a CTA the tile's other part is always done by then) adds the partials in the contributors'
 // order, activates and stores.
 //
 // While the last tiles are finished nothing is left to load, so the producer
@@ -167,6 +169,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gb + misc_off + 4);
     volatile int *n_groups = reinterpret_cast<volatile int *>(gb + misc_off + 8);
     volatile int *last_flag = reinterpret_cast<volatile int *>(gb + misc_off + 12);
+    volatile int *early_flag = reinterpret_cast<volatile int *>(gb + misc_off + 16);  // [2]
     uint32_t *tok_mask = reinterpret_cast<uint32_t *>(gb + misc_off + 24);  // [2][4]
     uint32_t *e_mask = tok_mask + 8;
     uint16_t *e_list = reinterpret_cast<uint16_t *>(e_mask + kMx4MaxExperts / 32);
@@ -348,6 +351,11 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             left -= kb1 - kb0;
             w.kb = KB - 1;
             w.next(KB, RT);
+            // a shared tile's contributors (worked out while the tile streams);
+            // only the first one's range may begin in an earlier tile
+            const int64_t ut = (static_cast<int64_t>(g) * RT + tile) * KB;
+            const int64_t cf = whole ? 0 : dec_owner(ut, U, C), cl = whole ? 0 : dec_owner(ut + KB - 1, U, C);
+            const int cf_slot = !whole && dec_start(cf, U, C) < ut;
             {
                 // the tokens that chose this expert
                 const int e = e_list[g];
@@ -358,14 +366,12 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
                 if (lane == 0)
                     tok_mask[wb * 4 + (et >> 5)] = m;
+                if (et == 0)
+                    early_flag[wb] = !whole && ld_acquire_gpu_u64(words + cf) == (kMx4Tag | static_cast<unsigned long long>(cl - cf));
                 dec_bar_sync();
             }
-            // a shared tile's contributors (worked out while the tile streams);
-            // only the first one's range may begin in an earlier tile
-            const int64_t ut = (static_cast<int64_t>(g) * RT + tile) * KB;
-            const int64_t cf = whole ? 0 : dec_owner(ut, U, C), cl = whole ? 0 : dec_owner(ut + KB - 1, U, C);
-            const int cf_slot = !whole && dec_start(cf, U, C) < ut;
             const uint32_t *mask = tok_mask + wb * 4;
+            const bool early = early_flag[wb];  // every other part of this tile is in the workspace
             wb ^= 1;
             // as in mx4_stream_kernel, a wait that gives up lets the warps go on
             bounded_wait(tfull_bar(acc), acc_phase, kErrWaitAccFull, abort_flag);
@@ -387,6 +393,37 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                     m &= m - 1;
                 }
             };
+            // sums over the contributors in their order, two partials in flight at a
+            // time; `own` (-1: none) is the one whose values gv, uv hold already
+            auto sum4 = [&](const int (&t)[4], int64_t own, float (&gv)[4], float (&uv)[4]) {
+                float sg[4] = {0.f, 0.f, 0.f, 0.f}, su[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int64_t c2 = cf; c2 <= cl; c2 += 2) {
+                    float a[2][4], b[2][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int64_t cs = min(c2 + k, cl);
+                        const float *p = ws + (cs * 2 + (cs == cf ? cf_slot : 0)) * SLOT + row;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool on = t[i] >= 0 && c2 + k <= cl && cs != own;
+                            a[k][i] = on ? __ldcg(p + t[i] * 128) : 0.0f;
+                            b[k][i] = on ? __ldcg(p + (BNX + t[i]) * 128) : 0.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            sg[i] += c2 + k == own ? gv[i] : a[k][i];
+                            su[i] += c2 + k == own ? uv[i] : b[k][i];
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    gv[i] = sg[i];
+                    uv[i] = su[i];
+                }
+            };
             if (inside) {
 #pragma unroll 1
                 for (int cc = 0; cc < BNX / 32; ++cc)
@@ -402,7 +439,9 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                             uv[i] = __uint_as_float(tmem_ld_32x32b_x1(col + BNX));
                         }
                         tmem_ld_wait();
-                        if (whole) {
+                        if (whole || early) {
+                            if (early)
+                                sum4(t, c, gv, uv);
                             mx4_store_h4(t, gv, uv, codes, I / 2, scale, zero_behind);
                         } else {
 #pragma unroll
@@ -422,42 +461,21 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 acc = 0;
                 acc_phase ^= 1u;
             }
-            if (whole)
+            if (whole || early)
                 continue;
             dec_bar_sync();  // this CTA's partial is written
             if (et == 0)
                 *last_flag = mx4_last_of(words + cf, static_cast<int>(cl - cf + 1));
             dec_bar_sync();
             if (*last_flag && inside) {
-                // their partials of two contributors in flight at a time
 #pragma unroll 1
                 for (int cc = 0; cc < BNX / 32; ++cc)
 #pragma unroll 1
                     for (uint32_t m = mask[cc]; m != 0u;) {
                         int t[4];
-                        float gv[4] = {0.f, 0.f, 0.f, 0.f}, uv[4] = {0.f, 0.f, 0.f, 0.f};
+                        float gv[4], uv[4];
                         take4(m, cc, t);
-                        for (int64_t c2 = cf; c2 <= cl; c2 += 2) {
-                            float a[2][4], b[2][4];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int64_t cs = min(c2 + k, cl);
-                                const float *p = ws + (cs * 2 + (cs == cf ? cf_slot : 0)) * SLOT + row;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const bool on = t[i] >= 0 && c2 + k <= cl;
-                                    a[k][i] = on ? __ldcg(p + t[i] * 128) : 0.0f;
-                                    b[k][i] = on ? __ldcg(p + (BNX + t[i]) * 128) : 0.0f;
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    gv[i] += a[k][i];
-                                    uv[i] += b[k][i];
-                                }
-                        }
+                        sum4(t, -1, gv, uv);
                         mx4_store_h4(t, gv, uv, codes, I / 2, scale, zero_behind);
                     }
             }
