@@ -216,8 +216,7 @@ __global__ void __launch_bounds__(kMx4PairThreads, 1)
                 const uint32_t shift = static_cast<uint32_t>(n_blk * BN % 128 / 32);
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     const int next = stage + 1 == STAGES ? 0 : stage + 1;
-                    if (!warp_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
-                        !warp_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                    if (!warp_wait2(full_bar(stage), scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
                         ok = false;
                         break;
                     }

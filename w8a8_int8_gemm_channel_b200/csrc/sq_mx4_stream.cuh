@@ -333,8 +333,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             tc_fence_after_sync();
             const uint32_t d = tmem_base + static_cast<uint32_t>(acc * Cfg::NACC * BNX);
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!warp_wait(full_bar(stage), phase, kErrWaitMma, abort_flag) ||
-                    !warp_wait(scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
+                if (!warp_wait2(full_bar(stage), scale_bar(stage), phase, kErrWaitMma, abort_flag)) {
                     ok = false;
                     break;
                 }

@@ -138,6 +138,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigne
     return __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity, code, abort_flag));
 }
 
+// Both of two barriers, looked at together (the second's code is the same).
+__device__ __forceinline__ bool warp_wait2(uint32_t a, uint32_t b, uint32_t parity, unsigned int code,
+                                           volatile int *abort_flag)
+{
+    const bool pa = mbar_try_wait(a, parity), pb = mbar_try_wait(b, parity);
+    if (__all_sync(0xFFFFFFFFu, pa && pb))
+        return true;
+    return warp_wait(a, parity, code, abort_flag) && warp_wait(b, parity, code, abort_flag);
+}
+
 // ----------------------------------------------------------------------------
 // thread-block clusters: rank, distributed shared memory, cluster barriers
 // ----------------------------------------------------------------------------
