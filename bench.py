@@ -616,11 +616,61 @@ def run_reference(args, rank, world):
 # single-call cases (per-kernel timing and profiler captures)
 # ---------------------------------------------------------------------------
 
+def mx4_case(kind, d, dev):
+    """(call, operations, bytes) of one microscaled 4-bit call on synthetic bf16 data."""
+    import w8a8_int8_gemm_channel_b200 as sq
+
+    per = 17 / 32  # bytes a value: a code and its share of the scale
+    u8, r = torch.uint8, lambda *shape: torch.randn(*shape, device=dev).to(torch.bfloat16)
+
+    def weight(*shape):
+        return sq.mx4_prepare_weight((torch.randn(*shape, device=dev) * 0.02).to(torch.bfloat16))
+
+    def done(f, *args):
+        f(*args)
+        return 0
+
+    if kind == "mx4_moe":
+        T, topk, E, H, I = d
+        xq, sx = sq.mx4_quantize(r(T, H))
+        route = torch.rand(T, E, device=dev).topk(topk, -1)
+        ids, w = route.indices.to(torch.int32).contiguous(), route.values.softmax(-1).contiguous()
+        experts = [t for shape in ((E, I, H), (E, I, H), (E, H, I)) for t in weight(*shape)]
+        y = torch.empty(T, H, device=dev, dtype=torch.bfloat16)
+        ws = torch.empty(sq.sq_mx4_moe_workspace_size(T, topk, E, H, I), dtype=u8, device=dev)
+        return (lambda: done(sq.sq_mx4_moe, xq, sx, ids, w, *experts, y, ws), 6 * T * topk * H * I,
+                ids.unique().numel() * 3 * H * I * per + T * H * (per + 2))
+    M, K = d[0], d[-1]
+    xq, sx = torch.empty(M, K // 2, dtype=u8, device=dev), torch.empty(sq.sq_mx4_scale_size(M, K), dtype=u8, device=dev)
+    if kind.startswith("residual_norm"):
+        b, res, out, gate = r(M, K), r(M, K), r(M, K), r(1, K)
+        gamma, g = torch.rand(K, device=dev) + 0.5, torch.rand(K, device=dev) + 0.5
+        if kind == "residual_norm":
+            xq, sx = torch.empty(M, K, dtype=torch.int8, device=dev), torch.empty(M, device=dev)
+        f = sq.sq_residual_norm_quant if kind == "residual_norm" else sq.sq_residual_norm_quant_mx4
+        return (lambda: done(f, b, gamma, gate, M, 1.0, res, out, g, 1e-5, xq, sx), 0,
+                M * K * (6 + (1 if kind == "residual_norm" else per)))
+    x, s = r(M, K), torch.rand(K, device=dev) + 0.5
+    if kind == "mx4_quant":
+        return lambda: done(sq.sq_mx4_quant_act, x, s, xq, sx), 0, M * K * (2 + per)
+    N = d[1]
+    wq, sw = weight(N, K)
+    y = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+    nbytes = N * K * per + 2 * M * N + M * K * (per if kind == "mx4_gemm" else 2)
+    if kind == "mx4_linear":
+        ws = torch.empty(sq.sq_mx4_linear_workspace_size(M, N, K), dtype=u8, device=dev)
+        return lambda: done(sq.sq_mx4_linear, x, s, wq, sw, y, ws), 2 * M * N * K, nbytes
+    sq.sq_mx4_quant_act(x, s, xq, sx)
+    ws = torch.empty(max(16, sq.sq_mx4_gemm_workspace_size(M, N, K)), dtype=u8, device=dev)
+    return lambda: done(sq.sq_mx4_gemm, xq, sx, wq, sw, y, ws), 2 * M * N * K, nbytes
+
+
 def run_case(spec, steps, warmup, flush_l2=True, settle_us=0.0):
     """Time one C-ABI call on synthetic data.  spec is one of
     gemm:M,N,K  linear:M,N,K  quant_act:M,K  quant_w:N,K  calib:T,K
     smooth_factors:N,K  rmsnorm_quant:M,K  silu_mul_quant:M,I  gptq_hessian:T,K  gptq_factor:K
-    gptq_rows:N,K  copy:bytes.  Prints one JSON line with the median time."""
+    gptq_rows:N,K  mx4_quant:M,K  mx4_gemm:M,N,K  mx4_linear:M,N,K  mx4_moe:T,topk,E,H,I
+    residual_norm:M,K (int8 codes)  residual_norm_mx4:M,K  copy:bytes.  Prints one JSON line with the median time."""
     import w8a8_int8_gemm_channel_b200 as sq
 
     lib = sq.lib()
@@ -731,6 +781,8 @@ def run_case(spec, steps, warmup, flush_l2=True, settle_us=0.0):
         fn = lambda: lib.sq_smooth_factors(ax.data_ptr(), w.data_ptr(), sq.SQ_BF16, N, K, 0.5,
                                            s.data_ptr(), None, st)
         nbytes = 2 * N * K + 8 * K
+    elif kind in ("mx4_quant", "mx4_gemm", "mx4_linear", "mx4_moe", "residual_norm", "residual_norm_mx4"):
+        fn, ops, nbytes = mx4_case(kind, d, dev)
     elif kind == "copy":
         # device-to-device copy of `bytes` bytes: the bandwidth a kernel of this size can reach
         (n,) = d

@@ -194,13 +194,16 @@ __device__ __forceinline__ void mx4_store_chunk(const float (&v)[8], bool in_k, 
         *word = byte;
 }
 
-// Zero scale bytes of the padding rows behind row `rows`: word i of them for
-// this thread and every `step`-th after it.
-__device__ __forceinline__ void mx4_zero_pad(uint8_t *scales, int64_t rows, int64_t KT, int64_t i, int64_t step)
+// Zero scale bytes of the padding rows behind row `rows` (at most 127 rows of KT
+// words, so 32-bit numbers hold them): word i of them for this thread and every
+// `step`-th after it.
+__device__ __forceinline__ void mx4_zero_pad(uint8_t *scales, int rows, int KT, unsigned i, unsigned step)
 {
-    const int64_t n = (((rows + 127) & ~int64_t{127}) - rows) * KT;
-    for (; i < n; i += step)
-        *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(rows + i / KT, i % KT, KT)) = 0u;
+    const unsigned n = static_cast<unsigned>(((rows + 127) & ~127) - rows) * static_cast<unsigned>(KT);
+    for (; i < n; i += step) {
+        const unsigned r = i / static_cast<unsigned>(KT);
+        *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(rows + static_cast<int>(r), i - r * KT, KT)) = 0u;
+    }
 }
 
 // Quantiser.  A thread owns 8 columns (its factors stay in registers) and walks
@@ -269,10 +272,11 @@ __global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restr
         px += xstep * U;
         pq += xstep / 2 * U;
     }
-    const int64_t nt = static_cast<int64_t>(gridDim.x) * gridDim.y * kMx4Threads;
-    const int64_t me = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kMx4Threads + threadIdx.x;
+    // (a grid has at most 2^24 threads: 8 CTAs an SM, or one for each 2048 columns)
+    const unsigned nt = gridDim.x * gridDim.y * kMx4Threads;
+    const unsigned me = (blockIdx.y * gridDim.x + blockIdx.x) * kMx4Threads + threadIdx.x;
     mx4_zero_pad(scales, rows, KT, me, nt);
-    for (int64_t i = me; i < nzero; i += nt)
+    for (int i = static_cast<int>(me); i < nzero; i += static_cast<int>(nt))
         zero[i] = 0;
 }
 

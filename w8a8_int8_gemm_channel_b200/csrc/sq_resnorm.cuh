@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) res_norm_kernel(const ResArgs
         }
     }
     if constexpr (MX4)
-        mx4_zero_pad(static_cast<uint8_t *>(p.sx), p.M, KT, static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x,
-                     static_cast<int64_t>(gridDim.x) * THREADS);
+        mx4_zero_pad(static_cast<uint8_t *>(p.sx), static_cast<int>(p.M), KT, blockIdx.x * THREADS + threadIdx.x,
+                     gridDim.x * THREADS);
 }
 
 }  // namespace sq
