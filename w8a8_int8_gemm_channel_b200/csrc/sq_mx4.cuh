@@ -211,9 +211,9 @@ __device__ __forceinline__ void mx4_zero_pad(uint8_t *scales, int rows, int KT, 
 // word of scale bytes.  A CTA covers TX * 8 columns, TX a multiple of 16, and 256
 // / TX rows at a time.  Memory-bound for fp32 (4096 x 8192 at 5.3 TB/s); with
 // bf16's 2.5 bytes a value the instructions count too, so the maximum takes three
-// operands an instruction and the products are packed.  (16 columns a thread
-// halve the shuffles but spread each load over twice the lines: 28672 x 4096 in
-// 94 us.)  The smoothing divides by multiplying with RN(1 / s), one division a
+// operands an instruction and the products are packed: 28672 x 4096 in 64 us, 4.6
+// TB/s.  (16 columns a thread halve the shuffles but spread each load over twice
+// the lines: 94 us.)  The smoothing divides by multiplying with RN(1 / s), one division a
 // column and band instead of one a value.
 // `zero`: tile counts of the product after it, cleared on the side.
 template <typename T, int OP>
@@ -292,7 +292,7 @@ __device__ __forceinline__ __half2 e2m1x2_to_half2(uint32_t byte)
 }
 
 // The values the codes stand for: 8 codes (4 bytes) a thread, U rows in flight,
-// the same walk as the quantiser.  E2M1 times a power of two is exact in fp32
+// the same walk as the quantiser (28672 x 4096 to bf16 in 61 us, 4.9 TB/s).  E2M1 times a power of two is exact in fp32
 // and in bf16 (subnormal ones included).
 template <typename T>
 __global__ void __launch_bounds__(kMx4Threads) mx4_dequant_kernel(const uint8_t *__restrict__ codes,

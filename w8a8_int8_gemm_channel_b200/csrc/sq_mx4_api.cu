@@ -326,10 +326,6 @@ sq_status check_mx4_moe_dims(int64_t T, int64_t topk, int64_t E, int64_t H, int6
     return SQ_OK;
 }
 
-// Units (17 KB) of the second half that a CTA of the first prefetches into L2 once
-// its own loads are out: 62 MB in all, half of the L2.
-constexpr int kMx4Ahead = 24;
-
 struct Mx4MoeCall {
     const uint8_t *xq, *sx, *wg, *sg, *wu, *su, *wd, *sd;
     sq::Mx4MoeArgs route;
@@ -365,8 +361,8 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
         return SQ_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(di.sms, kMx4MaxCtas));
     sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), Up::SMEM_BYTES, st, 0, 0,
-                                tg, tsg, tu, tsu, tx, tsx, td, tsd, hq, hs, slots, c.route.words, cnt, static_cast<int>(c.T),
-                                static_cast<int>(c.H), static_cast<int>(c.I), kMx4Ahead, c.route);
+                                tg, tsg, tu, tsu, tx, tsx, hq, hs, slots, c.route.words, cnt, static_cast<int>(c.T),
+                                static_cast<int>(c.H), static_cast<int>(c.I), c.route);
     if (r != SQ_OK)
         return r;
     constexpr int stages = BNX == 128 ? 6 : 8;

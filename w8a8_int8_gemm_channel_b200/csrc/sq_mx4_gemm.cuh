@@ -19,9 +19,12 @@
 // takes the whole accumulator into registers (eight warps, half the columns
 // each) and frees it, and stores while the next tile multiplies.
 //
-// Bound: the 1 kW power cap.  8192 x 8192 x 28672 runs at 4.8 PFLOP/s held (1.40
-// GHz, tensor pipe 70% busy) and 5.5 in a burst; without its operand loads the
-// same loop makes 6.5 at 1.85 GHz, without the scale copies as well 8.3.
+// Bound: the operands' way from L2 (11 TB/s at 256 wide) and, held, the 1 kW power
+// cap.  8192 x 8192 x 28672 runs at 4.8 PFLOP/s held (1.44 GHz) and 5.5 in a burst,
+// 4096 x 6144 x 4096 at 4.2; without its operand loads the same loop makes 6.5 at
+// 1.85 GHz, without the scale copies as well 8.3.  An MMA of N = 128 takes as long
+// as one of 256 (some 130 cycles), so narrow tiles are for few rounds only.
+// Groups of 8 m blocks (4, 16, 32: 811, 811, 895 us against 786).
 #pragma once
 
 #include <cstdint>

@@ -23,13 +23,20 @@
 // to hide the loaded memory's latency; two experts of 4096 x 14336 took 38 us.)
 //
 // A tile that several CTAs share is summed through the workspace; the last of
-// them (mx4_last_of, or before that a look at the count while its part still
-// streams, which spares it writing and counting its own partial: with fewer k
-// blocks a tile than units a CTA the tile's other part is always done by then) adds the partials in the contributors'
-// order, activates and stores.
+// them (mx4_last_of) adds the partials in the contributors' order, activates and
+// stores.  A look at the count while its part still streams spares it writing and
+// counting its own partial where the others are done already, as they are when a
+// tile has fewer k blocks than a CTA units (64 tokens, 48 of 64 experts of 2048 x
+// 1408: 80 -> 78 us the layer).
 //
-// While the last tiles are finished nothing is left to load, so the producer
-// prefetches the first units of this CTA's range of the second half into L2.
+// Measured (B200, calls one after another, this kernel and the second half): one
+// token, 2 experts of 4096 x 14336, 46 us; 16 tokens, 80 experts of 2048 x 768, 55
+// us; 64 tokens, 64 experts of 2048 x 1408, 77 us; the weights alone take 29, 32 and
+// 45 us at the copy rate.  This kernel streams at 5 to 6 TB/s once it runs; what
+// is left is fixed: finding the experts (1.3 us), the first loads (2 to 6 us),
+// the boundary between the halves (4 us) and the shared tiles at the ends (3 to 8
+// us).  Prefetching the second half's weights into L2 from here, two warps
+// issuing the MMAs, and four instead of two partials in flight changed nothing.
 //
 // Roles as in mx4_stream_kernel.  The gate and the up product are two
 // accumulators in the same lanes, so a thread holds both values of its channel,
@@ -140,10 +147,9 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     mx4_moe_up_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmSG,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmSU,
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
-                      const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmSD,
                       uint8_t *__restrict__ hq, uint8_t *__restrict__ hs, float *__restrict__ ws,
                       unsigned long long *__restrict__ words, int *__restrict__ cnt, int M, int H, int I,
-                      int ahead, Mx4MoeArgs moe)
+                      Mx4MoeArgs moe)
 {
     using Cfg = Mx4UpCfg<BNX>;
     constexpr int STAGES = Cfg::STAGES;
@@ -246,18 +252,6 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 if (++stage == STAGES) {
                     stage = 0;
                     phase ^= 1u;
-                }
-            }
-            // the down projection's units, as mx4_stream_kernel cuts them
-            const int T = (H + 127) / 128, KBD = (I + kMx4KB - 1) / kMx4KB;
-            const int64_t UD = static_cast<int64_t>(G) * T * KBD, CD = min(static_cast<int64_t>(gridDim.x), UD);
-            if (c < CD && !*abort_flag) {
-                const int64_t d0 = dec_start(c, UD, CD);
-                Mx4Unit d(d0, static_cast<int64_t>(G) * KBD, KBD);
-                for (int i = static_cast<int>(min(dec_start(c + 1, UD, CD) - d0, static_cast<int64_t>(ahead))); i > 0; --i) {
-                    tma_prefetch_l2_2d(&tmD, d.kb * 128, e_list[d.g] * H + d.t * 128);
-                    tma_prefetch_l2_3d(&tmSD, 0, d.kb * 2, e_list[d.g] * T + d.t);
-                    d.next(KBD, G);
                 }
             }
         }
