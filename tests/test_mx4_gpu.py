@@ -136,3 +136,19 @@ def test_linear(M, N, K, dtype):
     first = y.clone()
     sq.sq_mx4_linear(x.cuda(), s.cuda(), wq, sw, y, ws)
     assert torch.equal(first, y)
+
+
+@pytest.mark.parametrize("M", [5, 40, 300])
+def test_nan_blocks_spoil_their_row_and_column_alone(M):
+    N, K = 272, 416
+    x, w = values(M, K, M), values(N, K, N, F32, 0.02)
+    clean = [sq.mx4_quantize(x.cuda()), sq.mx4_prepare_weight(w.cuda())]
+    x[3, 64] = float("nan")
+    w[9, 400] = float("inf")
+    dirty = [sq.mx4_quantize(x.cuda()), sq.mx4_prepare_weight(w.cuda())]
+    a, b = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    sq.sq_mx4_gemm(*clean[0], *clean[1], a)
+    sq.sq_mx4_gemm(*dirty[0], *dirty[1], b)
+    assert torch.isnan(b[3]).all() and torch.isnan(b[:, 9]).all()
+    rows, cols = [i for i in range(M) if i != 3], [j for j in range(N) if j != 9]
+    assert torch.equal(a[rows][:, cols], b[rows][:, cols])
