@@ -120,6 +120,25 @@ __device__ __forceinline__ int mx4_active_experts(const int *__restrict__ ids, i
     return *count;
 }
 
+// How many of `grid` CTAs share the work of `tiles` tiles of `per_tile` units: all
+// of them, the units cut evenly wherever that falls, or S for each tile (S = 1:
+// nothing is summed), whichever the estimate says is done first.  Times in ns: a
+// unit's, a shared tile's fixed part, and what each contributor adds to its sum.
+// (54 tokens, 4 experts of 2656 x 320, cut into ranges of one unit whatever the sums
+// cost: 92 us.)  All lanes of a converged warp call it; lane S - 1 looks at S.
+__device__ __forceinline__ int mx4_share(int tiles, int per_tile, int grid, int unit, int fixed, int each)
+{
+    const int s = (threadIdx.x & 31) + 1;
+    const bool fits = s <= per_tile && static_cast<int64_t>(s) * tiles <= grid;
+    const int split = (per_tile + s - 1) / s * unit + (s > 1 ? fixed + each * s : 0);
+    const unsigned best = __reduce_min_sync(0xFFFFFFFFu, fits ? static_cast<unsigned>(min(split, 1 << 25)) << 6 | s : ~0u);
+    const int64_t units = static_cast<int64_t>(tiles) * per_tile;
+    const int64_t range = (units + grid - 1) / grid;
+    const int64_t even = range * unit + fixed + each * (per_tile / max(range, int64_t{1}) + 2);
+    return best == ~0u || even <= static_cast<int64_t>(best >> 6) ? static_cast<int>(min(static_cast<int64_t>(grid), units))
+                                                                  : static_cast<int>(best & 63u) * tiles;
+}
+
 // The scale tiles of one operand's stage into its 8 TMEM columns; `steps` MMAs
 // of 64 values are inside K, two a tile.
 __device__ __forceinline__ void mx4_copy_scales(uint32_t taddr, uint32_t saddr, int steps)
@@ -269,7 +288,8 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     const int KB = (K + kMx4KB - 1) / kMx4KB;
     const int64_t per_tile = static_cast<int64_t>(G) * KB;  // units of a tile
     const int64_t U = T * per_tile;
-    const int64_t C = min(static_cast<int64_t>(ctas), U);  // CTAs with work
+    const int64_t C = MOE ? mx4_share(T, G * KB, ctas, 320, 2500, M > 32 ? 500 : 150)
+                          : min(static_cast<int64_t>(ctas), U);  // CTAs with work
     const int64_t c = blockIdx.x;
     const bool works = c < C;
     const int64_t u0 = works ? dec_start(c, U, C) : 0, u1 = works ? dec_start(c + 1, U, C) : 0;
