@@ -360,7 +360,7 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
         !make_tmap_mx4(&th, hq, c.L.groups * c.T, c.I, BNX) || !make_tmap_scales(&tsh, hs, c.L.groups, c.I, 1))
         return SQ_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(di.sms, kMx4MaxCtas));
-    sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), Up::SMEM_BYTES, st, 0, 0,
+    sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4UpThreads), Up::SMEM_BYTES, st, 0, 0,
                                 tg, tsg, tu, tsu, tx, tsx, hq, hs, slots, c.route.words, cnt, static_cast<int>(c.T),
                                 static_cast<int>(c.H), static_cast<int>(c.I), c.route);
     if (r != SQ_OK)

@@ -121,6 +121,11 @@ __device__ __forceinline__ float mx4_silu(float v)
     return fmaf(fmaf(-q, d, n), r, q);
 }
 
+constexpr int kMx4UpThreads = 352;
+
+// the epilogue warps' barrier
+__device__ __forceinline__ void up_bar_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
+
 // Four tokens (t < 0: none) of every lane's channel: activates, quantises over the
 // 32 lanes and stores codes and scale byte.  Written once and looped over the
 // chosen tokens: unrolled over all of a tile's columns, the instruction fetches
@@ -160,7 +165,7 @@ __device__ __forceinline__ void mx4_store_h4(const int (&t)[4], const float (&g)
 }
 
 template <int BNX>
-__global__ void __launch_bounds__(kMx4StreamThreads, 1)
+__global__ void __launch_bounds__(kMx4UpThreads, 1)
     mx4_moe_up_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmSG,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmSU,
                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 4);  // the 4 epilogue warps
+            mbar_init(tempty_bar(b), 8);  // the 8 epilogue warps
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -349,10 +354,12 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 bounded_wait(scale_bar(last), last_phase, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
         }
     } else {
-        // epilogue warps 3..6: warp w holds block w % 4 of the tile, a channel a lane
+        // epilogue warps 3..10: warp w holds block w % 4 of the tile, a channel a lane;
+        // 3..6 and 7..10 take the tile's chosen tokens in turn, four at a time
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const int et = threadIdx.x - 96;
+        const int set = et >> 7;
         constexpr int SLOT = 2 * BNX * 128;  // floats of a partial tile: [gate, up][token][row]
         int acc = 0, wb = 0;
         uint32_t acc_phase = 0;
@@ -370,17 +377,19 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             const int cf_slot = !whole && dec_start(cf, U, C) < ut;
             {
                 // the tokens that chose this expert
-                const int e = e_list[g];
-                bool has = false;
-                if (et < M)
-                    for (int k = 0; k < moe.topk; ++k)
-                        has = has || chosen[et * moe.topk + k] == e;
-                const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
-                if (lane == 0)
-                    tok_mask[wb * 4 + (et >> 5)] = m;
+                if (set == 0) {
+                    const int e = e_list[g];
+                    bool has = false;
+                    if (et < M)
+                        for (int k = 0; k < moe.topk; ++k)
+                            has = has || chosen[et * moe.topk + k] == e;
+                    const uint32_t m = __ballot_sync(0xFFFFFFFFu, has);
+                    if (lane == 0)
+                        tok_mask[wb * 4 + (et >> 5)] = m;
+                }
                 if (et == 0)
                     early_flag[wb] = !whole && ld_acquire_gpu_u64(words + cf) == (kMx4Tag | static_cast<unsigned long long>(cl - cf));
-                dec_bar_sync();
+                up_bar_sync();
             }
             const uint32_t *mask = tok_mask + wb * 4;
             const bool early = early_flag[wb];  // every other part of this tile is in the workspace
@@ -437,6 +446,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                 }
             };
             if (inside) {
+                int turn = set;
 #pragma unroll 1
                 for (int cc = 0; cc < BNX / 32; ++cc)
 #pragma unroll 1
@@ -444,6 +454,8 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                         int t[4];
                         float gv[4], uv[4];
                         take4(m, cc, t);
+                        if (turn++ & 1)
+                            continue;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t col = lane_addr + static_cast<uint32_t>(max(t[i], 0));
@@ -475,11 +487,12 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
             }
             if (whole || early)
                 continue;
-            dec_bar_sync();  // this CTA's partial is written
+            up_bar_sync();  // this CTA's partial is written
             if (et == 0)
                 *last_flag = mx4_last_of(words + cf, static_cast<int>(cl - cf + 1));
-            dec_bar_sync();
+            up_bar_sync();
             if (*last_flag && inside) {
+                int turn = set;
 #pragma unroll 1
                 for (int cc = 0; cc < BNX / 32; ++cc)
 #pragma unroll 1
@@ -487,11 +500,13 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
                         int t[4];
                         float gv[4], uv[4];
                         take4(m, cc, t);
+                        if (turn++ & 1)
+                            continue;
                         sum4(t, -1, gv, uv);
                         mx4_store_h4(t, gv, uv, codes, I / 2, scale, zero_behind);
                     }
             }
-            dec_bar_sync();  // last_flag is rewritten by the next shared tile
+            up_bar_sync();  // last_flag is rewritten by the next shared tile
         }
     }
 
