@@ -121,36 +121,42 @@ __device__ __forceinline__ float mx4_silu(float v)
     return fmaf(fmaf(-q, d, n), r, q);
 }
 
-constexpr int kMx4UpThreads = 352;
+// Epilogue warps of the first half: sets of four.  A token's channels of one block
+// are a chain of a maximum, a quantisation and three shuffles, mostly latency: one
+// set with four tokens at a time took 46 tokens, 40 experts of 384 x 6112 in 87 us
+// and 128 tokens, 16 experts of 2048 x 1024 in 57, two sets 81 and 51, four sets 77
+// and 49, and four with two tokens at a time 72 and 48.
+constexpr int kMx4UpSets = 4;
+constexpr int kMx4UpThreads = 96 + kMx4UpSets * 128;
 
 // the epilogue warps' barrier
-__device__ __forceinline__ void up_bar_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
+__device__ __forceinline__ void up_bar_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kMx4UpSets * 128) : "memory"); }
 
-// Four tokens (t < 0: none) of every lane's channel: activates, quantises over the
+// Two tokens (t < 0: none) of every lane's channel: activates, quantises over the
 // 32 lanes and stores codes and scale byte.  Written once and looped over the
 // chosen tokens: unrolled over all of a tile's columns, the instruction fetches
 // took longer than the work.
-__device__ __forceinline__ void mx4_store_h4(const int (&t)[4], const float (&g)[4], const float (&u)[4], uint8_t *codes,
+__device__ __forceinline__ void mx4_store_h2(const int (&t)[2], const float (&g)[2], const float (&u)[2], uint8_t *codes,
                                              int row_bytes, uint8_t *scale, int zero_behind)
 {
     const int lane = threadIdx.x & 31;
-    float h[4];
-    uint32_t byte[4], c[4];
+    float h[2];
+    uint32_t byte[2], c[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
         h[i] = mx4_silu(g[i]) * u[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         byte[i] = mx4_scale_byte(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h[i]) & 0x7FFFFFFFu)));
         c[i] = byte[i] == 255u ? 0u : mx4_code1(h[i] * mx4_inv_scale(byte[i])) << (4 * (lane & 7));
     }
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
             c[i] |= __shfl_xor_sync(0xFFFFFFFFu, c[i], d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         if (t[i] < 0)
             continue;
         if ((lane & 7) == 0)
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull_bar(b), 1);
-            mbar_init(tempty_bar(b), 8);  // the 8 epilogue warps
+            mbar_init(tempty_bar(b), 4 * kMx4UpSets);  // the 16 epilogue warps
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -354,8 +360,8 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
                 bounded_wait(scale_bar(last), last_phase, kErrWaitDrain, nullptr, kWaitTimeoutNs / 4);
         }
     } else {
-        // epilogue warps 3..10: warp w holds block w % 4 of the tile, a channel a lane;
-        // 3..6 and 7..10 take the tile's chosen tokens in turn, four at a time
+        // epilogue warps 3..18: warp w holds block w % 4 of the tile, a channel a lane;
+        // the four sets of four warps take the tile's chosen tokens in turn, two at a time
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const int et = threadIdx.x - 96;
@@ -406,26 +412,26 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
             float *mine = ws + (c * 2 + (g == first.t && tile == first.g ? 0 : 1)) * SLOT;
             const uint32_t lane_addr =
                 tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * 2 * BNX);
-            // four chosen tokens at a time
-            auto take4 = [](uint32_t &m, int cc, int (&t)[4]) {
+            // two chosen tokens at a time
+            auto take2 = [](uint32_t &m, int cc, int (&t)[2]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     t[i] = m != 0u ? cc * 32 + __ffs(m) - 1 : -1;
                     m &= m - 1;
                 }
             };
             // sums over the contributors in their order, two partials in flight at a
             // time; `own` (-1: none) is the one whose values gv, uv hold already
-            auto sum4 = [&](const int (&t)[4], int64_t own, float (&gv)[4], float (&uv)[4]) {
-                float sg[4] = {0.f, 0.f, 0.f, 0.f}, su[4] = {0.f, 0.f, 0.f, 0.f};
+            auto sum2 = [&](const int (&t)[2], int64_t own, float (&gv)[2], float (&uv)[2]) {
+                float sg[2] = {}, su[2] = {};
                 for (int64_t c2 = cf; c2 <= cl; c2 += 2) {
-                    float a[2][4], b[2][4];
+                    float a[2][2], b[2][2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int64_t cs = min(c2 + k, cl);
                         const float *p = ws + (cs * 2 + (cs == cf ? cf_slot : 0)) * SLOT + row;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             const bool on = t[i] >= 0 && c2 + k <= cl && cs != own;
                             a[k][i] = on ? __ldcg(p + t[i] * 128) : 0.0f;
                             b[k][i] = on ? __ldcg(p + (BNX + t[i]) * 128) : 0.0f;
@@ -434,30 +440,30 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             sg[i] += c2 + k == own ? gv[i] : a[k][i];
                             su[i] += c2 + k == own ? uv[i] : b[k][i];
                         }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     gv[i] = sg[i];
                     uv[i] = su[i];
                 }
             };
             if (inside) {
-                int turn = set;
+                int turn = kMx4UpSets - set;
 #pragma unroll 1
                 for (int cc = 0; cc < BNX / 32; ++cc)
 #pragma unroll 1
                     for (uint32_t m = mask[cc]; m != 0u;) {
-                        int t[4];
-                        float gv[4], uv[4];
-                        take4(m, cc, t);
-                        if (turn++ & 1)
+                        int t[2];
+                        float gv[2], uv[2];
+                        take2(m, cc, t);
+                        if (turn++ % kMx4UpSets != 0)
                             continue;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             const uint32_t col = lane_addr + static_cast<uint32_t>(max(t[i], 0));
                             gv[i] = __uint_as_float(tmem_ld_32x32b_x1(col));
                             uv[i] = __uint_as_float(tmem_ld_32x32b_x1(col + BNX));
@@ -465,11 +471,11 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
                         tmem_ld_wait();
                         if (whole || early) {
                             if (early)
-                                sum4(t, c, gv, uv);
-                            mx4_store_h4(t, gv, uv, codes, I / 2, scale, zero_behind);
+                                sum2(t, c, gv, uv);
+                            mx4_store_h2(t, gv, uv, codes, I / 2, scale, zero_behind);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 2; ++i)
                                 if (t[i] >= 0) {
                                     mine[t[i] * 128 + row] = gv[i];
                                     mine[(BNX + t[i]) * 128 + row] = uv[i];
@@ -492,18 +498,18 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
                 *last_flag = mx4_last_of(words + cf, static_cast<int>(cl - cf + 1));
             up_bar_sync();
             if (*last_flag && inside) {
-                int turn = set;
+                int turn = kMx4UpSets - set;
 #pragma unroll 1
                 for (int cc = 0; cc < BNX / 32; ++cc)
 #pragma unroll 1
                     for (uint32_t m = mask[cc]; m != 0u;) {
-                        int t[4];
-                        float gv[4], uv[4];
-                        take4(m, cc, t);
-                        if (turn++ & 1)
+                        int t[2];
+                        float gv[2], uv[2];
+                        take2(m, cc, t);
+                        if (turn++ % kMx4UpSets != 0)
                             continue;
-                        sum4(t, -1, gv, uv);
-                        mx4_store_h4(t, gv, uv, codes, I / 2, scale, zero_behind);
+                        sum2(t, -1, gv, uv);
+                        mx4_store_h2(t, gv, uv, codes, I / 2, scale, zero_behind);
                     }
             }
             up_bar_sync();  // last_flag is rewritten by the next shared tile
