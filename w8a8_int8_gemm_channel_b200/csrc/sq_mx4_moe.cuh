@@ -30,15 +30,15 @@
 // 1408: 80 -> 78 us the layer).
 //
 // Measured (B200, calls one after another, this kernel and the second half): one
-// token, 2 experts of 4096 x 14336, 46 us; 16 tokens, 80 experts of 2048 x 768, 55
-// us; 64 tokens, 64 experts of 2048 x 1408, 77 us; the weights alone take 29, 32 and
+// token, 2 experts of 4096 x 14336, 46 us; 16 tokens, 80 experts of 2048 x 768, 53
+// us; 64 tokens, 64 experts of 2048 x 1408, 72 us; the weights alone take 29, 32 and
 // 45 us at the copy rate.  This kernel streams at 5 to 6 TB/s once it runs; what
 // is left is fixed: finding the experts (1.3 us), the first loads (2 to 6 us),
 // the boundary between the halves (4 us) and the shared tiles at the ends (3 to 8
 // us).  Prefetching the second half's weights into L2 from here, two warps
 // issuing the MMAs, and four instead of two partials in flight changed nothing.
 //
-// Roles as in mx4_stream_kernel.  The gate and the up product are two
+// Roles as in mx4_stream_kernel, with 16 epilogue warps (kMx4UpSets).  The gate and the up product are two
 // accumulators in the same lanes, so a thread holds both values of its channel,
 // and a warp the 32 channels of one block of the quantised h.
 #pragma once
@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
         cnt[blockIdx.x] = 0;
     const int RT = (I + 127) / 128, KB = (H + kMx4KB - 1) / kMx4KB;
     const int64_t U = static_cast<int64_t>(G) * RT * KB;
-    // CTAs with work; a tile has M * topk / G tokens on average, summed four at a time
+    // CTAs with work; a contributor costs 400 ns for every four tokens of a tile, which
+    // has M * topk / G on average
     const int64_t C = mx4_share(G * RT, KB, static_cast<int>(gridDim.x), 850, 2500,
                                 400 * ((M * moe.topk / max(G, 1) + 3) / 4));
     const int64_t c = blockIdx.x;
