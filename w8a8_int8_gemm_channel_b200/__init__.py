@@ -32,9 +32,14 @@ The raw entry points keep the C names and take caller-allocated outputs:
 
 ``calibrate``, ``prepare_weight`` and ``linear`` are conveniences that allocate
 their outputs with torch and call the raw entry points.
+
+With ``stream=`` (a torch stream or a raw handle) a call runs there instead of on
+the current stream, and what it allocates, workspaces and outputs, belongs to
+that stream: wait for it before an output is used on another one.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -202,6 +207,28 @@ def _stream(stream=None) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, device):
+    """Context in which torch allocates and fills on the stream that a call is launched on.  A tensor allocated on the
+    current stream may be written there by earlier work, and is given to later work there as soon as it is dropped: both
+    while `stream` uses it."""
+    if stream is None:
+        return _HERE
+    torch = _torch()
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)  # 0 and 1 name the legacy default stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _scratch(nbytes: int, device, stream):
+    torch = _torch()
+    with _on(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 # ---------------------------------------------------------------------------
 # raw entry points (C names)
 # ---------------------------------------------------------------------------
@@ -262,12 +289,10 @@ def sq_gptq_hessian(x, s, H, stream=None):
 
 def sq_gptq_factor(H, U, damp_frac=0.01, workspace=None, stream=None):
     """Damps H in place and writes U, the upper Cholesky factor of H^-1."""
-    import torch
-
     K = H.shape[0]
     need = int(lib().sq_gptq_workspace_size(K))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=H.device)
+        workspace = _scratch(need, H.device, stream)
     _check("sq_gptq_factor", lib().sq_gptq_factor(_ptr(H), K, float(damp_frac), _ptr(U), _ptr(workspace),
                                                   workspace.numel() * workspace.element_size(), _stream(stream)))
 
@@ -282,16 +307,16 @@ def sq_gptq_quant_weight(w, s, U, wq, sw, stream=None):
 def gptq_weight(xcal, w, s, damp_frac=0.01, stream=None):
     """GPTQ in place of prepare_weight's plain rounding: (wq, sw) for the
     smoothed weight w * s, with the Hessian from the calibration tokens xcal."""
-    import torch
-
+    torch = _torch()
     K = w.shape[1]
-    H = torch.empty(K, K, dtype=torch.float64, device=w.device)
-    U = torch.empty_like(H)
-    sq_gptq_hessian(xcal, s, H, stream)
-    sq_gptq_factor(H, U, damp_frac, stream=stream)
-    wq = torch.empty(w.shape, dtype=torch.int8, device=w.device)
-    sw = torch.empty(w.shape[0], dtype=torch.float32, device=w.device)
-    sq_gptq_quant_weight(w, s, U, wq, sw, stream)
+    with _on(stream, w.device):
+        H = torch.empty(K, K, dtype=torch.float64, device=w.device)
+        U = torch.empty_like(H)
+        sq_gptq_hessian(xcal, s, H, stream)
+        sq_gptq_factor(H, U, damp_frac, stream=stream)
+        wq = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+        sw = torch.empty(w.shape[0], dtype=torch.float32, device=w.device)
+        sq_gptq_quant_weight(w, s, U, wq, sw, stream)
     return wq, sw
 
 
@@ -309,12 +334,10 @@ def sq_w8a8_gemm_workspace_size(M: int, N: int, K: int) -> int:
 
 def sq_w8a8_gemm_ws(xq, sx, wq, sw, y, workspace=None, stream=None):
     """sq_w8a8_gemm with a workspace (allocated here when not given)."""
-    import torch
-
     M, K = xq.shape
     N = wq.shape[0]
     if workspace is None:
-        workspace = torch.empty(sq_w8a8_gemm_workspace_size(M, N, K), dtype=torch.uint8, device=xq.device)
+        workspace = _scratch(sq_w8a8_gemm_workspace_size(M, N, K), xq.device, stream)
     _check("sq_w8a8_gemm_ws",
            lib().sq_w8a8_gemm_ws(_ptr(xq), _ptr(sx), _ptr(wq), _ptr(sw), M, N, K, _ptr(y), _dtype_code(y),
                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -464,7 +487,7 @@ def sq_mx4_gemm(xq, sx, wq, sw, y, workspace=None, stream=None):
     M, N = y.shape
     K = xq.shape[1] * 2
     if workspace is None:
-        workspace = _torch().empty(sq_mx4_gemm_workspace_size(M, N, K), dtype=_torch().uint8, device=y.device)
+        workspace = _scratch(sq_mx4_gemm_workspace_size(M, N, K), y.device, stream)
     _call("sq_mx4_gemm", stream, (y, xq, sx, wq, sw, workspace),
           lambda: (*_mx4_ptrs(M, K, xq, sx), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(), _code(y),
                    *_ws_args(workspace)))
@@ -481,7 +504,7 @@ def sq_mx4_linear(x, s, wq, sw, y, workspace=None, stream=None):
     if y.shape != (M, N):
         raise ValueError(f"y: shape {(M, N)}")
     if workspace is None:
-        workspace = _torch().empty(sq_mx4_linear_workspace_size(M, N, K), dtype=_torch().uint8, device=x.device)
+        workspace = _scratch(sq_mx4_linear_workspace_size(M, N, K), x.device, stream)
     _call("sq_mx4_linear", stream, (x, s, wq, sw, y, workspace),
           lambda: (x.data_ptr(), _code(x), _mx4_factors(s, K), *_mx4_ptrs(N, K, wq, sw), M, N, K, y.data_ptr(),
                    _code(y), *_ws_args(workspace)))
@@ -509,7 +532,7 @@ def sq_mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, y, workspace=None, 
     if y.shape != (T, H):
         raise ValueError(f"y: shape {(T, H)}")
     if workspace is None:
-        workspace = torch.empty(sq_mx4_moe_workspace_size(T, topk, E, H, I), dtype=u8, device=y.device)
+        workspace = _scratch(sq_mx4_moe_workspace_size(T, topk, E, H, I), y.device, stream)
     _call("sq_mx4_moe", stream, (y, xq, sx, ids, weights, wg, sg, wu, su, wd, sd, workspace),
           lambda: (*_mx4_ptrs(T, H, xq, sx), ids.data_ptr(), weights.data_ptr(), T, topk, E, H, I, wg.data_ptr(),
                    sg.data_ptr(), wu.data_ptr(), su.data_ptr(), wd.data_ptr(), sd.data_ptr(), y.data_ptr(),
@@ -562,9 +585,10 @@ def calibrate(x_batches, K: Optional[int] = None, stream=None):
     torch = _torch()
     batches = [x_batches] if hasattr(x_batches, "shape") else list(x_batches)
     K = K or batches[0].shape[1]
-    ax = torch.zeros(K, dtype=torch.float32, device=batches[0].device)
-    for b in batches:
-        sq_calib_absmax(b, ax, stream)
+    with _on(stream, batches[0].device):
+        ax = torch.zeros(K, dtype=torch.float32, device=batches[0].device)
+        for b in batches:
+            sq_calib_absmax(b, ax, stream)
     return ax
 
 
@@ -572,11 +596,12 @@ def prepare_weight(ax, w, alpha: float, stream=None):
     """Smoothing factors and the smoothed int8 weight: returns (s, wq, sw)."""
     torch = _torch()
     N, K = w.shape
-    s = torch.empty(K, dtype=torch.float32, device=w.device)
-    sq_smooth_factors(ax, w, alpha, s, None, stream)
-    wq = torch.empty(N, K, dtype=torch.int8, device=w.device)
-    sw = torch.empty(N, dtype=torch.float32, device=w.device)
-    sq_smooth_quant_weight(w, s, wq, sw, stream)
+    with _on(stream, w.device):
+        s = torch.empty(K, dtype=torch.float32, device=w.device)
+        sq_smooth_factors(ax, w, alpha, s, None, stream)
+        wq = torch.empty(N, K, dtype=torch.int8, device=w.device)
+        sw = torch.empty(N, dtype=torch.float32, device=w.device)
+        sq_smooth_quant_weight(w, s, wq, sw, stream)
     return s, wq, sw
 
 
@@ -585,11 +610,12 @@ def linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
     torch = _torch()
     M, K = x.shape
     N = wq.shape[0]
-    y = torch.empty(M, N, dtype=out_dtype or x.dtype, device=x.device)
-    need = sq_linear_workspace_size(M, N, K)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    sq_linear(x, s, wq, sw, y, workspace if need else None, stream)
+    with _on(stream, x.device):
+        y = torch.empty(M, N, dtype=out_dtype or x.dtype, device=x.device)
+        need = sq_linear_workspace_size(M, N, K)
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        sq_linear(x, s, wq, sw, y, workspace if need else None, stream)
     return y
 
 
@@ -597,8 +623,9 @@ def mx4_quantize(x, s=None, stream=None):
     """Codes and scale tiles of the activations x [M, K], divided by s when given: returns (xq, sx)."""
     torch = _torch()
     M, K = x.shape
-    xq = torch.empty(M, K // 2, dtype=torch.uint8, device=x.device)
-    sx = torch.empty(sq_mx4_scale_size(M, K), dtype=torch.uint8, device=x.device)
+    with _on(stream, x.device):
+        xq = torch.empty(M, K // 2, dtype=torch.uint8, device=x.device)
+        sx = torch.empty(sq_mx4_scale_size(M, K), dtype=torch.uint8, device=x.device)
     sq_mx4_quant_act(x, s, xq, sx, stream)
     return xq, sx
 
@@ -608,8 +635,9 @@ def mx4_prepare_weight(w, s=None, stream=None):
     returns (wq, sw), [N, K / 2] and [bytes] or [E, N, K / 2] and [E, bytes]."""
     torch = _torch()
     N, K = w.shape[-2:]
-    wq = torch.empty(*w.shape[:-1], K // 2, dtype=torch.uint8, device=w.device)
-    sw = torch.empty(*w.shape[:-2], sq_mx4_scale_size(N, K), dtype=torch.uint8, device=w.device)
+    with _on(stream, w.device):
+        wq = torch.empty(*w.shape[:-1], K // 2, dtype=torch.uint8, device=w.device)
+        sw = torch.empty(*w.shape[:-2], sq_mx4_scale_size(N, K), dtype=torch.uint8, device=w.device)
     for one, q, sc in zip(*(t.reshape(-1, *t.shape[-d:]) for t, d in ((w, 2), (wq, 2), (sw, 1)))):
         sq_mx4_quant_weight(one, s, q, sc, stream)
     return wq, sw
@@ -617,7 +645,8 @@ def mx4_prepare_weight(w, s=None, stream=None):
 
 def mx4_linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
     """y = mx4(x / s) w^T with a torch-allocated output."""
-    y = _torch().empty(x.shape[0], wq.shape[0], dtype=out_dtype or x.dtype, device=x.device)
+    with _on(stream, x.device):
+        y = _torch().empty(x.shape[0], wq.shape[0], dtype=out_dtype or x.dtype, device=x.device)
     sq_mx4_linear(x, s, wq, sw, y, workspace, stream)
     return y
 
@@ -625,6 +654,7 @@ def mx4_linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
 def mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, out_dtype=None, workspace=None, stream=None):
     """A few tokens through their experts with a torch-allocated output (bfloat16 unless out_dtype says otherwise)."""
     torch = _torch()
-    y = torch.empty(ids.shape[0], wd.shape[1], dtype=out_dtype or torch.bfloat16, device=xq.device)
+    with _on(stream, xq.device):
+        y = torch.empty(ids.shape[0], wd.shape[1], dtype=out_dtype or torch.bfloat16, device=xq.device)
     sq_mx4_moe(xq, sx, ids, weights, wg, sg, wu, su, wd, sd, y, workspace, stream)
     return y
