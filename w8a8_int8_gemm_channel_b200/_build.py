@@ -9,6 +9,7 @@ tree).  cudart is linked statically; only the ABI symbols are exported.
 """
 from __future__ import annotations
 
+import contextlib
 import os
 import re
 import shutil
@@ -22,7 +23,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsq.so")
 MAIN = os.path.join(CSRC, "sq_api.cu")
 UNITS = [MAIN, os.path.join(CSRC, "sq_mx4_api.cu")]
-OBJ = os.path.join(PKG, "_build.d")  # object files, kept between builds (their names hold the process id until done)
+# object files, kept between builds (their names hold the process id until done), and the flags that they and the
+# library were made with
+OBJ = os.path.join(PKG, "_build.d")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = [
@@ -48,11 +51,39 @@ def sources():
     ) + [os.path.join(INCLUDE, "sq.h")]
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def _flags(path, extra=None) -> str:
+    """The flags an object, or the library, is made with."""
+    return " ".join([*NVCC_FLAGS, *(extra or []), *(LINK_FLAGS if path == LIB else [])])
+
+
+def _flags_file(path):
+    return os.path.join(OBJ, os.path.basename(path) + ".flags")
+
+
+def _older(path, files, extra) -> bool:
+    """Whether a built file is missing, older than one of the files, or made with other flags."""
+    if not os.path.exists(path) or not os.path.exists(_flags_file(path)):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in sources())
+    with open(_flags_file(path)) as f:
+        if f.read() != _flags(path, extra):
+            return True
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(s) > t for s in files)
+
+
+def _place(tmp, path, extra):
+    """A finished file takes its name; without its flags it counts as missing, so they come last."""
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(_flags_file(path))
+    os.replace(tmp, path)
+    new = _flags_file(path) + f".tmp{os.getpid()}"
+    with open(new, "w") as f:
+        f.write(_flags(path, extra))
+    os.replace(new, _flags_file(path))
+
+
+def stale(extra=None) -> bool:
+    return _older(LIB, sources(), extra)
 
 
 def _headers(unit, seen=None):
@@ -73,22 +104,16 @@ def _object(unit):
     return os.path.join(OBJ, os.path.basename(unit)[:-3] + ".o")
 
 
-def _object_stale(unit) -> bool:
-    obj = _object(unit)
-    if not os.path.exists(obj):
-        return True
-    t = os.path.getmtime(obj)
-    return any(os.path.getmtime(s) > t for s in [unit, *_headers(unit)])
+def _object_stale(unit, extra=None) -> bool:
+    return _older(_object(unit), [unit, *_headers(unit)], extra)
 
 
-def build(force: bool = False, verbose: bool = False, extra=None) -> str:
-    """Compile libsq.so if it is missing or older than any source; return its path."""
-    if not force and not stale():
-        return LIB
+def objects(force: bool = False, verbose: bool = False, extra=None) -> list:
+    """Compile the units whose objects are stale; return the objects' paths."""
     os.makedirs(OBJ, exist_ok=True)
     running = []
     for unit in UNITS:
-        if force or extra or _object_stale(unit):
+        if force or _object_stale(unit, extra):
             tmp = _object(unit) + f".tmp{os.getpid()}.o"
             cmd = [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, "-c", "-o", tmp, unit]
             if verbose:
@@ -99,15 +124,23 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         if p.wait() != 0:
             failed = failed or subprocess.CalledProcessError(p.returncode, cmd)
         else:
-            os.replace(tmp, obj)
+            _place(tmp, obj, extra)
     if failed:
         raise failed
+    return [_object(unit) for unit in UNITS]
+
+
+def build(force: bool = False, verbose: bool = False, extra=None) -> str:
+    """Compile libsq.so if it is missing, older than any source or made with other flags; return its path."""
+    if not force and not stale(extra):
+        return LIB
+    objs = objects(force, verbose, extra)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-o", tmp, *map(_object, UNITS), *LINK_FLAGS]
+    cmd = [nvcc(), *ARCH, "-o", tmp, *objs, *LINK_FLAGS]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    _place(tmp, LIB, extra)
     return LIB
 
 
