@@ -502,7 +502,9 @@ SQ_API sq_status sq_residual_norm_quant_mx4(const void *b, sq_dtype dt, int64_t 
  * sq_gptq_factor meets a non-positive pivot.  Returns SQ_OK, SQ_ERR_TIMEOUT
  * (a wait gave up), SQ_ERR_INVALID_ARG (code 0xA00: the GPTQ Hessian was not
  * positive definite), with the kernel's location code in *code when code is
- * not NULL, or SQ_ERR_CUDA if the synchronisation itself failed.
+ * not NULL, or SQ_ERR_CUDA if the synchronisation itself failed.  Where a wait
+ * of an MXFP4 kernel and a pivot are both pending, the wait is reported and the
+ * pivot stays for the next call.
  */
 SQ_API sq_status sq_device_status(sq_stream_t stream, uint32_t *code);
 

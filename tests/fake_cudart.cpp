@@ -1,0 +1,139 @@
+// A stand-in for the CUDA runtime, for tests of the library's host code on a
+// machine without a GPU: launches are noted and return, device variables live in
+// their host shadows, and a launch can be made to fail.
+#include <cstring>
+#include <string>
+#include <vector>
+
+#include <cuda_runtime_api.h>
+
+namespace {
+
+struct Launch {
+    std::string name;
+    unsigned grid;
+    const void *arg0;
+    int arg1;
+};
+
+std::vector<std::pair<const void *, std::string>> functions, variables;
+std::vector<Launch> launches;
+int fail_at = -1;
+cudaError_t last = cudaSuccess;
+void *handle = nullptr;
+
+int encode_tiled() { return 0; }
+
+std::string name_of(const void *f)
+{
+    for (auto &p : functions)
+        if (p.first == f)
+            return p.second;
+    return "?";
+}
+
+}  // namespace
+
+extern "C" {
+
+// ---- what the tests ask ---------------------------------------------------------
+void fake_reset(int fail)  // the launch number `fail` fails (-1: none)
+{
+    launches.clear();
+    fail_at = fail;
+    last = cudaSuccess;
+}
+int fake_launches() { return static_cast<int>(launches.size()); }
+const char *fake_launch_name(int i) { return launches[i].name.c_str(); }
+unsigned fake_launch_grid(int i) { return launches[i].grid; }
+const void *fake_launch_arg0(int i) { return launches[i].arg0; }
+int fake_launch_arg1(int i) { return launches[i].arg1; }
+// the i-th device variable whose name holds `part`
+void *fake_variable(const char *part, int i)
+{
+    for (auto &p : variables)
+        if (p.second.find(part) != std::string::npos && i-- == 0)
+            return const_cast<void *>(p.first);
+    return nullptr;
+}
+
+// ---- the runtime ------------------------------------------------------------------
+void **__cudaRegisterFatBinary(void *) { return &handle; }
+void __cudaRegisterFatBinaryEnd(void **) {}
+void __cudaUnregisterFatBinary(void **) {}
+void __cudaRegisterFunction(void **, const char *host, char *, const char *name, int, uint3 *, uint3 *, dim3 *, dim3 *, int *)
+{
+    functions.emplace_back(host, name);
+}
+void __cudaRegisterVar(void **, char *host, char *, const char *name, int, size_t, int, int)
+{
+    variables.emplace_back(host, name);
+}
+unsigned __cudaPopCallConfiguration(dim3 *, dim3 *, size_t *, void *) { return cudaErrorInvalidConfiguration; }
+
+cudaError_t cudaGetDevice(int *d)
+{
+    *d = 0;
+    return cudaSuccess;
+}
+cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr a, int)
+{
+    *v = a == cudaDevAttrMultiProcessorCount ? 148 : 0;
+    return cudaSuccess;
+}
+cudaError_t cudaFuncSetAttribute(const void *, cudaFuncAttribute, int) { return cudaSuccess; }
+cudaError_t cudaGetDriverEntryPoint(const char *, void **f, unsigned long long, cudaDriverEntryPointQueryResult *r)
+{
+    *f = reinterpret_cast<void *>(&encode_tiled);
+    *r = cudaDriverEntryPointSuccess;
+    return cudaSuccess;
+}
+cudaError_t cudaGetLastError()
+{
+    const cudaError_t e = last;
+    last = cudaSuccess;
+    return e;
+}
+cudaError_t cudaPeekAtLastError() { return last; }
+cudaError_t cudaGetSymbolAddress(void **p, const void *symbol)
+{
+    *p = const_cast<void *>(symbol);
+    return cudaSuccess;
+}
+cudaError_t cudaLaunchKernel(const void *, dim3, dim3, void **, size_t, cudaStream_t) { return last = cudaErrorLaunchFailure; }
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const void *f, void **args)
+{
+    Launch l{name_of(f), c->gridDim.x, nullptr, 0};
+    if (l.name.find("clear") != std::string::npos) {  // (int *, int)
+        std::memcpy(&l.arg0, args[0], sizeof l.arg0);
+        std::memcpy(&l.arg1, args[1], sizeof l.arg1);
+    }
+    launches.push_back(l);
+    if (fake_launches() - 1 == fail_at)
+        return last = cudaErrorLaunchOutOfResources;
+    return cudaSuccess;
+}
+cudaError_t cudaMemcpyFromSymbol(void *dst, const void *symbol, size_t n, size_t offset, cudaMemcpyKind)
+{
+    std::memcpy(dst, static_cast<const char *>(symbol) + offset, n);
+    return cudaSuccess;
+}
+cudaError_t cudaMemcpyToSymbol(const void *symbol, const void *src, size_t n, size_t offset, cudaMemcpyKind)
+{
+    std::memcpy(static_cast<char *>(const_cast<void *>(symbol)) + offset, src, n);
+    return cudaSuccess;
+}
+cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int *n, const void *, int, size_t, unsigned)
+{
+    *n = 1;
+    return cudaSuccess;
+}
+cudaError_t cudaOccupancyMaxActiveClusters(int *n, const void *, const cudaLaunchConfig_t *c)
+{
+    *n = 148 / 2;
+    (void)c;
+    return cudaSuccess;
+}
+cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
+
+}  // extern "C"

@@ -1503,19 +1503,21 @@ sq_status sq_device_status(sq_stream_t stream, uint32_t *code)
         cudaGetLastError();
         return SQ_ERR_CUDA;
     }
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&v, sq::g_sq_device_error, sizeof v) != cudaSuccess ||
-        cudaMemcpyToSymbol(sq::g_sq_device_error, &zero, sizeof zero) != cudaSuccess) {
+    unsigned int v8 = 0, v4 = 0;
+    const unsigned int zero = 0;
+    if (cudaMemcpyFromSymbol(&v8, sq::g_sq_device_error, sizeof v8) != cudaSuccess ||
+        sq::mx4_read_device_error(&v4) != cudaSuccess) {
         cudaGetLastError();
         return SQ_ERR_CUDA;
     }
-    unsigned int v4 = 0;
-    if (sq::mx4_take_device_error(&v4) != cudaSuccess) {
+    // a wait that gave up comes before a pivot, which stays for the next call then
+    const bool behind = v8 == sq::kErrGptqPivot && v4 != 0;
+    const unsigned int v = v8 == 0 || behind ? v4 : v8;
+    if ((v8 != 0 && !behind && cudaMemcpyToSymbol(sq::g_sq_device_error, &zero, sizeof zero) != cudaSuccess) ||
+        (v4 != 0 && sq::mx4_clear_device_error() != cudaSuccess)) {
         cudaGetLastError();
         return SQ_ERR_CUDA;
     }
-    if (v == 0)
-        v = v4;
     if (code != nullptr)
         *code = v;
     if (v == 0)

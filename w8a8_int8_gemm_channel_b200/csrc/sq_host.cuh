@@ -21,8 +21,9 @@
 
 namespace sq {
 
-// Reads and clears the error word of the other translation unit (sq_mx4_api.cu).
-cudaError_t mx4_take_device_error(unsigned int *code);
+// Read and clear the error word of the other translation unit (sq_mx4_api.cu).
+cudaError_t mx4_read_device_error(unsigned int *code);
+cudaError_t mx4_clear_device_error();
 
 }  // namespace sq
 

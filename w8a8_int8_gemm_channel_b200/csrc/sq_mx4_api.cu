@@ -19,13 +19,15 @@
 
 namespace sq {
 
-cudaError_t mx4_take_device_error(unsigned int *code)
+cudaError_t mx4_read_device_error(unsigned int *code)
 {
-    unsigned int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_sq_device_error, sizeof *code);
-    if (e == cudaSuccess)
-        e = cudaMemcpyToSymbol(g_sq_device_error, &zero, sizeof zero);
-    return e;
+    return cudaMemcpyFromSymbol(code, g_sq_device_error, sizeof *code);
+}
+
+cudaError_t mx4_clear_device_error()
+{
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_sq_device_error, &zero, sizeof zero);
 }
 
 }  // namespace sq
