@@ -41,3 +41,51 @@ def test_no_pending_error_is_lost(lib):
             assert st == k and code in (int8, mx4) and kind[code] == k, (int8, mx4)
         assert status(lib) == (sq.SQ_OK, 0)
         assert [w.value for w in words(lib)] == [0, 0]
+
+
+WS = 0x7F0000100000
+
+
+def moe(lib, T=4, topk=2, E=8, H=256, I=160):
+    """An experts layer on fake addresses, which nothing reads: (status, address of the tile words)."""
+    A = 0x7F0000001000
+    size = lib.sq_mx4_moe_workspace_size(T, topk, E, H, I)
+    st = lib.sq_mx4_moe(A, A, A, A, T, topk, E, H, I, A, A, A, A, A, A, A, sq.SQ_BF16, WS, size, None)
+    groups = min(E, T * topk)
+    return st, WS + -(-groups * T * I // 2 // 256) * 256 + groups * lib.sq_mx4_scale_size(1, I)
+
+
+def test_experts_layer_whose_second_half_is_not_launched(lib):
+    """The first half counts in words that the second half sets back.  Where that one cannot be launched they are
+    cleared, or the next call on the workspace would go by what this one counted."""
+    lib.fake_reset(-1)
+    assert moe(lib)[0] == sq.SQ_OK
+    names = fake_cuda.launches(lib)
+    assert len(names) == 2 and "moe_up" in names[0] and "stream" in names[1]
+    for fails in (0, 1):
+        lib.fake_reset(fails)
+        st, words = moe(lib)
+        names = fake_cuda.launches(lib)
+        assert st == sq.SQ_ERR_CUDA
+        assert len(names) == fails + 2 and "clear" in names[-1], names
+        last = len(names) - 1
+        assert lib.fake_launch_arg0(last) == words
+        assert lib.fake_launch_arg1(last) * 4 >= 8 * lib.fake_launch_grid(0)  # a word for each CTA
+    lib.fake_reset(-1)
+    assert moe(lib)[0] == sq.SQ_OK  # nothing of the error is left
+
+
+def test_a_launch_that_fails_is_reported(lib):
+    A, size = 0x7F0000001000, 1 << 40
+    calls = [lambda: lib.sq_mx4_linear(A, 1, A, A, A, 8, 256, 256, A, 1, WS, size, None),
+             lambda: lib.sq_mx4_gemm(A, A, A, A, 8, 256, 256, A, 1, WS, size, None),
+             lambda: lib.sq_mx4_gemm(A, A, A, A, 300, 256, 256, A, 1, WS, size, None),
+             lambda: lib.sq_mx4_quant_weight(A, 0, 8, 256, None, A, A, None),
+             lambda: lib.sq_residual_norm_quant(A, 1, 8, 256, A, None, 1, 1.0, A, WS, A, 1e-5, A, A, None)]
+    for call in calls:
+        lib.fake_reset(-1)
+        assert call() == sq.SQ_OK
+        n = lib.fake_launches()
+        for fails in range(n):
+            lib.fake_reset(fails)
+            assert call() == sq.SQ_ERR_CUDA and lib.fake_launches() == fails + 1

@@ -365,14 +365,22 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
     sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4UpThreads), Up::SMEM_BYTES, st, 0, 0,
                                 tg, tsg, tu, tsu, tx, tsx, hq, hs, slots, c.route.words, cnt, static_cast<int>(c.T),
                                 static_cast<int>(c.H), static_cast<int>(c.I), c.route);
+    // what the first half counts is set back by the second; without that one the
+    // next call on this workspace would go by it
+    auto uncounted = [&](sq_status err) {
+        launch_kernel(mx4_clear_kernel, dim3(1), dim3(kMx4MaxCtas), 0, st, 0, 0, reinterpret_cast<int *>(c.route.words),
+                      static_cast<int>(kMx4Words / sizeof(int)));
+        return err;
+    };
     if (r != SQ_OK)
-        return r;
+        return uncounted(r);
     constexpr int stages = BNX == 128 ? 6 : 8;
     constexpr int smem = sq::mx4_stream_smem(Cfg::STAGE_BYTES, stages, true);
     static_assert(smem <= kMaxDynSmem && stages <= Cfg::MAX_STAGES, "shared memory");
-    return launch_kernel(down, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), smem, st, 0, 0, td, tsd, th, tsh,
-                         c.y, slots, cnt, static_cast<int>(c.T), static_cast<int>(c.H), static_cast<int>(c.I), ctas,
-                         stages, 1, c.route);
+    r = launch_kernel(down, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4StreamThreads), smem, st, 0, 0, td, tsd, th, tsh,
+                      c.y, slots, cnt, static_cast<int>(c.T), static_cast<int>(c.H), static_cast<int>(c.I), ctas,
+                      stages, 1, c.route);
+    return r == SQ_OK ? r : uncounted(r);
 }
 
 template <int OUT>
