@@ -151,3 +151,27 @@ def test_a_token_with_nan_spoils_itself_alone():
     assert torch.isnan(z[2]).all()
     keep = [i for i in range(T) if i != 2]
     assert torch.equal(y[keep], z[keep])
+
+
+@pytest.mark.parametrize("below", [0, 1, 2, 3, 70000])
+def test_workspace_contents_around_the_counts_tag(below):
+    """A workspace of words that a few adds turn into tagged ones (and of what a finished call leaves, 0 below)."""
+    T, topk, E, H, I = 2, 2, 64, 2048, 1408  # three CTAs a tile of the first half
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def matrix(*shape):  # any codes, every scale 1/16
+        return [torch.randint(0, 256, (*shape[:-1], shape[-1] // 2), generator=g, dtype=torch.uint8, device="cuda"),
+                torch.full((*shape[:-2], sq.sq_mx4_scale_size(*shape[-2:])), 123, dtype=torch.uint8, device="cuda")]
+
+    ids = torch.tensor([[3, 60], [17, 41]], dtype=torch.int32, device="cuda")
+    t = [*matrix(T, H), ids, torch.rand(T, topk, generator=g, device="cuda"), *matrix(E, I, H), *matrix(E, I, H), *matrix(E, H, I)]
+    n = sq.sq_mx4_moe_workspace_size(T, topk, E, H, I)
+    y = [torch.empty(T, H, device="cuda") for _ in range(2)]
+    sq.sq_mx4_moe(*t, y[0], torch.zeros(n, dtype=torch.uint8, device="cuda"))
+    assert torch.isfinite(y[0]).all() and (y[0] != 0).any()
+    tag = (0x9E3779B97F4A << 16) - below
+    ws = torch.full((n // 8,), tag - (1 << 64), dtype=torch.int64, device="cuda").view(torch.uint8)
+    assert ws.numel() == n
+    for _ in range(2):
+        sq.sq_mx4_moe(*t, y[1], ws)
+        assert torch.equal(*y)

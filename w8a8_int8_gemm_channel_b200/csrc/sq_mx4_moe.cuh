@@ -75,13 +75,16 @@ struct Mx4UpCfg {
 // finds it swaps in (tag, 1), or (tag, n + 1) where another one was faster; what
 // was added to it before that is lost with it.  Release and acquire: the partials
 // written before (ordered by the caller's barrier) are visible to the last one.
+// (Contents that become the tag by an add are no exception: whoever finds the tag
+// counts from what stands there, and everyone else swaps.)
 __device__ __forceinline__ bool mx4_last_of(unsigned long long *word, int total)
 {
     unsigned long long seen = atom_add_acq_rel_gpu_u64(word, 1ull), count;
     if ((seen & ~0xFFFFull) == kMx4Tag) {
         count = (seen & 0xFFFFu) + 1;
     } else {
-        for (;;) {  // a failed swap means that another contributor came between: at most 2 * total of them
+        ++seen;     // as the add left it
+        for (;;) {  // a failed swap means that another contributor added or swapped in between: at most 2 * total times
             count = (seen & ~0xFFFFull) == kMx4Tag ? (seen & 0xFFFFu) + 1 : 1;
             const unsigned long long old = atom_cas_acq_rel_gpu(word, seen, kMx4Tag | count);
             if (old == seen)
