@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restr
         px += xstep * U;
         pq += xstep / 2 * U;
     }
-    // (a grid has at most 2^24 threads: 8 CTAs an SM, or one for each 2048 columns)
+    // (a grid has at most 2^24 threads: 8 CTAs an SM, or one CTA for each 256 columns of at most 2^24)
     const unsigned nt = gridDim.x * gridDim.y * kMx4Threads;
     const unsigned me = (blockIdx.y * gridDim.x + blockIdx.x) * kMx4Threads + threadIdx.x;
     mx4_zero_pad(scales, rows, KT, me, nt);
