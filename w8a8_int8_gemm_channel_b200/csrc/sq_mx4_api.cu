@@ -362,6 +362,15 @@ sq_status launch_mx4_moe(const Mx4MoeCall &c, cudaStream_t st)
         !make_tmap_mx4(&th, hq, c.L.groups * c.T, c.I, BNX) || !make_tmap_scales(&tsh, hs, c.L.groups, c.I, 1))
         return SQ_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(di.sms, kMx4MaxCtas));
+    if (debug_plan()) {  // with as many experts in use as there can be (the kernels know how many there are)
+        const int G = static_cast<int>(c.L.groups), T = static_cast<int>(c.T), topk = c.route.topk;
+        const int ut = G * static_cast<int>(RI), un = static_cast<int>((c.H + sq::kMx4KB - 1) / sq::kMx4KB);
+        const int dt = static_cast<int>(RH), dn = G * static_cast<int>((c.I + sq::kMx4KB - 1) / sq::kMx4KB);
+        std::fprintf(stderr, "sq mx4 moe T=%d topk=%d E=%lld H=%lld I=%lld: BNX=%d experts=%d up tiles=%d units=%d ctas=%d "
+                     "down tiles=%d units=%d ctas=%d\n", T, topk, (long long)E, (long long)c.H, (long long)c.I, BNX, G, ut, un,
+                     sq::mx4_share_on_host(ut, un, ctas, sq::mx4_up_cost(T, topk, G)), dt, dn,
+                     sq::mx4_share_on_host(dt, dn, ctas, sq::mx4_down_cost(T)));
+    }
     sq_status r = launch_kernel(up, dim3(static_cast<unsigned>(ctas)), dim3(sq::kMx4UpThreads), Up::SMEM_BYTES, st, 0, 0,
                                 tg, tsg, tu, tsu, tx, tsx, hq, hs, slots, c.route.words, cnt, static_cast<int>(c.T),
                                 static_cast<int>(c.H), static_cast<int>(c.I), c.route);

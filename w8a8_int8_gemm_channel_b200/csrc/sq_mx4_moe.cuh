@@ -249,10 +249,7 @@ __global__ void __launch_bounds__(kMx4UpThreads, 1)
         cnt[blockIdx.x] = 0;
     const int RT = (I + 127) / 128, KB = (H + kMx4KB - 1) / kMx4KB;
     const int64_t U = static_cast<int64_t>(G) * RT * KB;
-    // CTAs with work; a contributor costs 400 ns for every four tokens of a tile, which
-    // has M * topk / G on average
-    const int64_t C = mx4_share(G * RT, KB, static_cast<int>(gridDim.x), 850, 2500,
-                                400 * ((M * moe.topk / max(G, 1) + 3) / 4));
+    const int64_t C = mx4_share(G * RT, KB, static_cast<int>(gridDim.x), mx4_up_cost(M, moe.topk, G));  // CTAs with work
     const int64_t c = blockIdx.x;
     const bool works = c < C;
     const int64_t u0 = works ? dec_start(c, U, C) : 0;

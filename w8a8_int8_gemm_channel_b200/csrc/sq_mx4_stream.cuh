@@ -125,18 +125,55 @@ __device__ __forceinline__ int mx4_active_experts(const int *__restrict__ ids, i
 // nothing is summed), whichever the estimate says is done first.  Times in ns: a
 // unit's, a shared tile's fixed part, and what each contributor adds to its sum.
 // (54 tokens, 4 experts of 2656 x 320, cut into ranges of one unit whatever the sums
-// cost: 92 us.)  All lanes of a converged warp call it; lane S - 1 looks at S.
-__device__ __forceinline__ int mx4_share(int tiles, int per_tile, int grid, int unit, int fixed, int each)
+// cost: 92 us.)
+struct Mx4Cost {
+    int unit, fixed, each;
+};
+
+// the first half: a contributor costs 400 ns for every four tokens of a tile, which
+// has M * topk / G on average
+__host__ __device__ __forceinline__ Mx4Cost mx4_up_cost(int M, int topk, int G)
 {
-    const int s = (threadIdx.x & 31) + 1;
-    const bool fits = s <= per_tile && static_cast<int64_t>(s) * tiles <= grid;
-    const int split = (per_tile + s - 1) / s * unit + (s > 1 ? fixed + each * s : 0);
-    const unsigned best = __reduce_min_sync(0xFFFFFFFFu, fits ? static_cast<unsigned>(min(split, 1 << 25)) << 6 | s : ~0u);
+    return {850, 2500, 400 * ((M * topk / (G > 1 ? G : 1) + 3) / 4)};
+}
+
+__host__ __device__ __forceinline__ Mx4Cost mx4_down_cost(int M) { return {320, 2500, M > 32 ? 500 : 150}; }
+
+// the estimate of S CTAs a tile and S itself in one number (~0: there are not as many)
+__host__ __device__ __forceinline__ unsigned mx4_split_key(int s, int tiles, int per_tile, int grid, Mx4Cost t)
+{
+    if (s > per_tile || static_cast<int64_t>(s) * tiles > grid)
+        return ~0u;
+    const int split = (per_tile + s - 1) / s * t.unit + (s > 1 ? t.fixed + t.each * s : 0);
+    return static_cast<unsigned>(split < 1 << 25 ? split : 1 << 25) << 6 | static_cast<unsigned>(s);
+}
+
+// the choice, `best` the least of the keys
+__host__ __device__ __forceinline__ int mx4_share_of(unsigned best, int tiles, int per_tile, int grid, Mx4Cost t)
+{
     const int64_t units = static_cast<int64_t>(tiles) * per_tile;
     const int64_t range = (units + grid - 1) / grid;
-    const int64_t even = range * unit + fixed + each * (per_tile / max(range, int64_t{1}) + 2);
-    return best == ~0u || even <= static_cast<int64_t>(best >> 6) ? static_cast<int>(min(static_cast<int64_t>(grid), units))
+    const int64_t even = range * t.unit + t.fixed + t.each * (per_tile / (range > 1 ? range : 1) + 2);
+    return best == ~0u || even <= static_cast<int64_t>(best >> 6) ? static_cast<int>(grid < units ? grid : units)
                                                                   : static_cast<int>(best & 63u) * tiles;
+}
+
+// All lanes of a converged warp call it; lane S - 1 looks at S.
+__device__ __forceinline__ int mx4_share(int tiles, int per_tile, int grid, Mx4Cost t)
+{
+    const int s = (threadIdx.x & 31) + 1;
+    return mx4_share_of(__reduce_min_sync(0xFFFFFFFFu, mx4_split_key(s, tiles, per_tile, grid, t)), tiles, per_tile, grid, t);
+}
+
+// The same on the host, for the printed plan.
+inline int mx4_share_on_host(int tiles, int per_tile, int grid, Mx4Cost t)
+{
+    unsigned best = ~0u;
+    for (int s = 1; s <= 32; ++s) {
+        const unsigned key = mx4_split_key(s, tiles, per_tile, grid, t);
+        best = key < best ? key : best;
+    }
+    return mx4_share_of(best, tiles, per_tile, grid, t);
 }
 
 // The scale tiles of one operand's stage into its 8 TMEM columns; `steps` MMAs
@@ -288,7 +325,7 @@ __global__ void __launch_bounds__(kMx4StreamThreads, 1)
     const int KB = (K + kMx4KB - 1) / kMx4KB;
     const int64_t per_tile = static_cast<int64_t>(G) * KB;  // units of a tile
     const int64_t U = T * per_tile;
-    const int64_t C = MOE ? mx4_share(T, G * KB, ctas, 320, 2500, M > 32 ? 500 : 150)
+    const int64_t C = MOE ? mx4_share(T, G * KB, ctas, mx4_down_cost(M))
                           : min(static_cast<int64_t>(ctas), U);  // CTAs with work
     const int64_t c = blockIdx.x;
     const bool works = c < C;
