@@ -140,3 +140,19 @@ def test_int8_ties_are_divided():
     q, sx, out = torch.empty(4, K, dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda"), torch.empty(4, K, device="cuda")
     sq.sq_residual_norm_quant(b.cuda(), None, None, 1, 1.0, r.cuda(), out, g.cuda(), 0.0, q, sx)
     assert np.array_equal(sx.cpu().numpy(), want_sx) and np.array_equal(q.cpu().numpy(), want_q)
+
+
+@pytest.mark.parametrize("M,K,dt", [(4, 32768, BF16), (130, 20032, BF16), (3, 32, F32), (700, 96, BF16), (600, 16416, BF16), (650, 16384, F32)])
+@pytest.mark.parametrize("post", [True, False])
+def test_longest_and_shortest_rows_mx4(M, K, dt, post):
+    b, gamma, gate, r, g = inputs(M, K, dt, K + 1, 3, post)
+    want_r, a = definition(b, gamma, gate, 3, -1.5, r, g, 1e-6, dt)
+    want_q, want_s, _ = mx4.quantize(a)
+    q = torch.full((M + 1, K // 2), 0xEE, dtype=torch.uint8, device="cuda")
+    sx = torch.full((sq.sq_mx4_scale_size(M, K) + 512,), 0xEE, dtype=torch.uint8, device="cuda")
+    out = torch.full((M + 1, K), 7.0, dtype=dt, device="cuda")
+    db, dgamma, dgate, dr, dg = cuda(b, gamma, gate, r, g)
+    sq.sq_residual_norm_quant_mx4(db, dgamma, dgate, 3, -1.5, dr, out[:M], dg, 1e-6, q[:M], sx[:-512])
+    assert torch.equal(out[:M].cpu(), want_r)
+    assert np.array_equal(sx[:-512].cpu().numpy(), want_s) and np.array_equal(q[:M].cpu().numpy(), want_q)
+    assert (out[M] == 7.0).all() and (q[M] == 0xEE).all() and (sx[-512:] == 0xEE).all()
