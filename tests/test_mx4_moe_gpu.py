@@ -175,3 +175,80 @@ def test_workspace_contents_around_the_counts_tag(below):
     for _ in range(2):
         sq.sq_mx4_moe(*t, y[1], ws)
         assert torch.equal(*y)
+
+
+def digits(v, n):
+    """Integers [rows] as E2M1 codes [rows, 32 n]: a hexadecimal digit in each block of 32, the lowest first."""
+    out = np.zeros((len(v), 32 * n), np.uint8)
+    for row, x in enumerate(v):
+        for i in range(n):
+            d, at = (int(x) >> 4 * i) & 15, 32 * i
+            while d:
+                part = max(p for p in (6, 4, 3, 2, 1) if p <= d)
+                out[row, at] = {1: 2, 2: 4, 3: 5, 4: 6, 6: 7}[part]
+                d, at = d - part, at + 1
+    return out
+
+
+def near_borders(count, low, high):
+    """(a, p, b, q, border, above): gate values a 2^p and up values b 2^q whose h = silu(gate) up lies between low and
+    high steps of 2^-24 from a border between two E2M1 values."""
+    rng = np.random.default_rng(12)
+    a = np.arange(2048, 4096)
+    exps = np.arange(-14, -5)  # |gate| from 1/8 to 64
+    A, P, S = (x.ravel() for x in np.meshgrid(a, exps, (1, -1), indexing="ij"))
+    g = S * A * 2.0 ** P
+    s = silu(g)
+    found = []
+    for border in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0):
+        m, e = np.frexp(border / np.abs(s))
+        b = np.rint(m * 65536)  # 16 bits
+        off = b / (m * 65536) - 1
+        hit = (np.abs(off) >= low * 2.0 ** -24) & (np.abs(off) <= high * 2.0 ** -24)
+        found += list(zip(S[hit] * A[hit], P[hit], b[hit].astype(np.int64), e[hit] - 16, np.full(hit.sum(), border), off[hit] > 0))
+    assert len(found) >= count
+    return [found[i] for i in rng.permutation(len(found))[:count]]
+
+
+def test_silu_is_as_accurate_as_it_says():
+    """The activation's error, up to 5 steps of 2^-24 and a little, and one of the product with up: an h that lies 6.5 to
+    13 such steps from a border has the code of its own side.  The gate and up products are exact here, and the down
+    projection hands h out as it is."""
+    n = 4096
+    levels = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+    cases = near_borders(n // 32 * 31, 6.5, 13.0)
+    cases = [c for i in range(n // 32) for c in [(2048, -5, 6 * 4096, -18, None, True), *cases[31 * i:31 * i + 31]]]
+    # each block's first channel: 64 times 6/64, which sets the scale to 1
+    a, p, b, q = (np.array([c[i] for c in cases]) for i in range(4))
+    codes = {"g": digits(np.abs(a), 3) | ((digits(np.abs(a), 3) != 0) * np.where(a < 0, 8, 0)[:, None]).astype(np.uint8), "u": digits(b, 4)}
+    at = mx4.tile_index(n, n)
+    t = {}
+    for k, base, num in (("g", p, 3), ("u", q, 4)):
+        nib = np.zeros((n, n), np.uint8)
+        nib[:, :32 * num] = codes[k]
+        tiles = np.full(mx4.scale_size(n, n), 127, np.uint8)
+        byte = 127 + base[:, None] + 4 * np.arange(num)
+        assert (byte > 0).all() and (byte < 255).all()
+        tiles[at[:, :num]] = byte
+        t[k] = (nib[:, 0::2] | (nib[:, 1::2] << 4), tiles)
+    g, u = (mx4.decode(t[k][0], t[k][1]).sum(1) for k in ("g", "u"))
+    assert np.array_equal(g, a * 2.0 ** p) and np.array_equal(u, b * 2.0 ** q)
+    h = silu(g) * u
+    want = []
+    for c, v in zip(cases, h):
+        border, above = c[4:]
+        assert border is None or abs(v) / border > 1 if above else abs(v) / border < 1
+        low = 7 if border is None else max(i for i in range(8) if levels[i] < border) + bool(above)
+        want.append(np.copysign(levels[low], v))
+    one = np.zeros((1, n), np.uint8)
+    one[:, :128] = 2
+    ident = np.zeros((n, n), np.uint8)
+    np.fill_diagonal(ident, 2)
+    pack = lambda c: c[:, 0::2] | (c[:, 1::2] << 4)  # noqa: E731
+    ones = lambda rows: np.full(mx4.scale_size(rows, n), 127, np.uint8)  # noqa: E731
+    args = [(pack(one), ones(1)), (t["g"][0][None], t["g"][1][None]), (t["u"][0][None], t["u"][1][None]), (pack(ident)[None], ones(n)[None])]
+    x, wg, wu, wd = [[torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in m] for m in args]
+    ids, weights = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, 1, device="cuda")
+    y = sq.mx4_moe(*x, ids, weights, *wg, *wu, *wd, out_dtype=F32).cpu().numpy()[0]
+    wrong = np.flatnonzero(y != np.array(want))
+    assert wrong.size == 0, [(cases[i], g[i], h[i], y[i]) for i in wrong[:5]]
