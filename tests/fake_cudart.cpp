@@ -1,7 +1,10 @@
 // A stand-in for the CUDA runtime, for tests of the library's host code on a
 // machine without a GPU: launches are noted and return, device variables live in
-// their host shadows, and a launch can be made to fail.
+// their host shadows, and launches, occupancy queries and allocations can be made
+// to fail.
+#include <cstdlib>
 #include <cstring>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -18,11 +21,18 @@ struct Launch {
 
 std::vector<std::pair<const void *, std::string>> functions, variables;
 std::vector<Launch> launches;
-int fail_at = -1;
+int fail_at = -1, fail_queries = 0;
+bool no_memory = false;
 cudaError_t last = cudaSuccess;
 void *handle = nullptr;
 
 int encode_tiled() { return 0; }
+
+struct Allow {  // the fake's own allocations
+    bool was = no_memory;
+    Allow() { no_memory = false; }
+    ~Allow() { no_memory = was; }
+};
 
 std::string name_of(const void *f)
 {
@@ -34,6 +44,16 @@ std::string name_of(const void *f)
 
 }  // namespace
 
+void *operator new(std::size_t n)
+{
+    void *p = no_memory ? nullptr : std::malloc(n);
+    if (p == nullptr)
+        throw std::bad_alloc();
+    return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, std::size_t) noexcept { std::free(p); }
+
 extern "C" {
 
 // ---- what the tests ask ---------------------------------------------------------
@@ -41,8 +61,12 @@ void fake_reset(int fail)  // the launch number `fail` fails (-1: none)
 {
     launches.clear();
     fail_at = fail;
+    fail_queries = 0;
+    no_memory = false;
     last = cudaSuccess;
 }
+void fake_fail_queries(int n) { fail_queries = n; }  // the next n occupancy queries fail
+void fake_no_memory(int on) { no_memory = on != 0; }  // operator new throws in the library's code
 int fake_launches() { return static_cast<int>(launches.size()); }
 const char *fake_launch_name(int i) { return launches[i].name.c_str(); }
 unsigned fake_launch_grid(int i) { return launches[i].grid; }
@@ -103,6 +127,7 @@ cudaError_t cudaGetSymbolAddress(void **p, const void *symbol)
 cudaError_t cudaLaunchKernel(const void *, dim3, dim3, void **, size_t, cudaStream_t) { return last = cudaErrorLaunchFailure; }
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const void *f, void **args)
 {
+    Allow a;
     Launch l{name_of(f), c->gridDim.x, nullptr, 0};
     if (l.name.find("clear") != std::string::npos) {  // (int *, int)
         std::memcpy(&l.arg0, args[0], sizeof l.arg0);
@@ -125,13 +150,16 @@ cudaError_t cudaMemcpyToSymbol(const void *symbol, const void *src, size_t n, si
 }
 cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int *n, const void *, int, size_t, unsigned)
 {
+    if (fail_queries > 0 && fail_queries-- > 0)
+        return last = cudaErrorInvalidValue;
     *n = 1;
     return cudaSuccess;
 }
-cudaError_t cudaOccupancyMaxActiveClusters(int *n, const void *, const cudaLaunchConfig_t *c)
+cudaError_t cudaOccupancyMaxActiveClusters(int *n, const void *, const cudaLaunchConfig_t *)
 {
+    if (fail_queries > 0 && fail_queries-- > 0)
+        return last = cudaErrorInvalidValue;
     *n = 148 / 2;
-    (void)c;
     return cudaSuccess;
 }
 cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }

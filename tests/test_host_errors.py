@@ -1,12 +1,16 @@
 """What the host code does about errors, on a stand-in for the CUDA runtime."""
 import ctypes
 import itertools
+import os
+import subprocess
+import sys
 
 import pytest
 
 import w8a8_int8_gemm_channel_b200 as sq
 from tests import fake_cuda
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PIVOT, WAIT, WAIT2 = 0xA00, 0x200, 0x400
 
 
@@ -89,3 +93,31 @@ def test_a_launch_that_fails_is_reported(lib):
         for fails in range(n):
             lib.fake_reset(fails)
             assert call() == sq.SQ_ERR_CUDA and lib.fake_launches() == fails + 1
+
+
+CHILD = """
+import sys, tempfile
+import w8a8_int8_gemm_channel_b200 as sq
+from tests import fake_cuda
+A = 0x7F0000001000
+with tempfile.TemporaryDirectory() as d:
+    lib = fake_cuda.load(d)
+    lib.fake_reset(-1)
+    lib.fake_no_memory(1)
+    calls = [lambda: lib.sq_mx4_gemm(A, A, A, A, 300, 256, 256, A, 1, A, 1 << 40, None),
+             lambda: lib.sq_quant_act(A, 1, 2000, 4096, A, A, A, None),
+             lambda: lib.sq_quant_act(A, 0, 2000, 1040, A, A, A, None),
+             lambda: lib.sq_silu_mul_quant(A, 1, 2000, 1040, A, A, A, None, None),
+             lambda: lib.sq_linear_noalloc(A, 1, A, A, A, 8, 256, 256, A, 1, None),
+             lambda: lib.sq_w8a8_gemm(A, A, A, A, 300, 256, 256, A, 1, None)]
+    got = [f() for f in calls]
+    lib.fake_no_memory(0)
+    print(got)
+"""
+
+
+def test_no_exception_leaves_the_library():
+    """Without host memory a call does its work or returns an error; an exception would end the process."""
+    out = subprocess.run([sys.executable, "-c", CHILD], cwd=ROOT, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    assert eval(out.stdout) == [sq.SQ_OK] * 6

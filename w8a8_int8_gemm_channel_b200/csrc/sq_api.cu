@@ -14,7 +14,6 @@
 #include <mutex>
 #include <tuple>
 #include <type_traits>
-#include <vector>
 #include <utility>
 #include <climits>
 
@@ -112,24 +111,16 @@ sq_status launch_row_quant_cfg(const T *in, int64_t rows, int64_t K, const float
     if (!ensure_smem_attr(kernel, kMaxDynSmem - 1024, attr_done))
         return SQ_ERR_CUDA;
     // resident CTAs per SM for this shared-memory size, cached per size
-    static std::mutex mu;
-    static std::vector<std::pair<int, int>> occ;  // smem -> CTAs per SM (one device type)
+    static Answers<int, 64> occ;  // smem -> CTAs per SM (one device type)
     int per_sm = 0;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        for (auto &e : occ)
-            if (e.first == smem)
-                per_sm = e.second;
-    }
-    if (per_sm == 0) {
+    if (!occ.find(smem, per_sm)) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, THREADS, smem) !=
                 cudaSuccess ||
             per_sm < 1) {
             cudaGetLastError();
             return SQ_ERR_CUDA;
         }
-        std::lock_guard<std::mutex> lk(mu);
-        occ.emplace_back(smem, per_sm);
+        occ.keep(smem, per_sm);
     }
     // few rows: spread each row over more warps so that every SM has work
     // (not for FIT, whose G is fixed by the row length)

@@ -14,7 +14,6 @@
 #include <cstdlib>
 #include <mutex>
 #include <utility>
-#include <vector>
 
 #include "sq.h"
 #include "sq_ptx.cuh"
@@ -177,27 +176,56 @@ bool ensure_smem_attr(KernelT kernel, int bytes, std::atomic<uint64_t> &done_mas
     return true;
 }
 
+// Answers of queries, kept by what was asked.  A fixed table: no allocation, so
+// nothing throws; what it has no room for is asked again.
+template <typename Key, int N>
+class Answers {
+    std::mutex mu_;
+    Key keys_[N];
+    int values_[N];
+    int n_ = 0;
+
+public:
+    bool find(const Key &k, int &value)
+    {
+        std::lock_guard<std::mutex> lk(mu_);
+        for (int i = 0; i < n_; ++i)
+            if (keys_[i] == k) {
+                value = values_[i];
+                return true;
+            }
+        return false;
+    }
+    void keep(const Key &k, int value)
+    {
+        std::lock_guard<std::mutex> lk(mu_);
+        if (n_ < N) {
+            keys_[n_] = k;
+            values_[n_++] = value;
+        }
+    }
+};
+
 // Clusters of `csize` CTAs of `threads` threads and `smem` bytes each that the
 // device can hold at once (cudaOccupancyMaxActiveClusters), cached per kernel
 // and shape.
 template <typename KernelT>
 int active_clusters(KernelT kernel, int csize, int smem, int threads)
 {
-    static std::mutex mu;
-    struct Entry {
+    struct Asked {
         const void *fn;
-        int dev, csize, smem, threads, n;
+        int dev, csize, smem, threads;
+        bool operator==(const Asked &o) const
+        {
+            return fn == o.fn && dev == o.dev && csize == o.csize && smem == o.smem && threads == o.threads;
+        }
     };
-    static std::vector<Entry> cache;
-    int dev = 0;
+    static Answers<Asked, 256> cache;
+    int dev = 0, n = 0;
     cudaGetDevice(&dev);
-    const void *fn = reinterpret_cast<const void *>(kernel);
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        for (auto &e : cache)
-            if (e.fn == fn && e.dev == dev && e.csize == csize && e.smem == smem && e.threads == threads)
-                return e.n;
-    }
+    const Asked asked{reinterpret_cast<const void *>(kernel), dev, csize, smem, threads};
+    if (cache.find(asked, n))
+        return n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(csize * 64));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -209,13 +237,11 @@ int active_clusters(KernelT kernel, int csize, int smem, int threads)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();
         n = 0;
     }
-    std::lock_guard<std::mutex> lk(mu);
-    cache.push_back(Entry{fn, dev, csize, smem, threads, n});
+    cache.keep(asked, n);
     return n;
 }
 
