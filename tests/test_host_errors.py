@@ -121,3 +121,15 @@ def test_no_exception_leaves_the_library():
     out = subprocess.run([sys.executable, "-c", CHILD], cwd=ROOT, capture_output=True, text=True)
     assert out.returncode == 0, out.stderr
     assert eval(out.stdout) == [sq.SQ_OK] * 6
+
+
+def test_a_failed_query_is_asked_again(lib):
+    """An occupancy query that fails once fails its call alone."""
+    A = 0x7F0000001000
+    calls = [lambda: lib.sq_mx4_gemm(A, A, A, A, 300, 256, 256, A, sq.SQ_F32, WS, 1 << 40, None),
+             lambda: lib.sq_w8a8_gemm(A, A, A, A, 2048, 4096, 4096, A, sq.SQ_F32, None)]
+    for call in calls:
+        lib.fake_reset(-1)
+        lib.fake_fail_queries(1)
+        assert call() == sq.SQ_ERR_CUDA and lib.fake_launches() == 0
+        assert call() == sq.SQ_OK and lib.fake_launches() > 0

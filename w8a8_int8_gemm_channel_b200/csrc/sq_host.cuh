@@ -208,7 +208,7 @@ public:
 
 // Clusters of `csize` CTAs of `threads` threads and `smem` bytes each that the
 // device can hold at once (cudaOccupancyMaxActiveClusters), cached per kernel
-// and shape.
+// and shape; 0 where the query fails.
 template <typename KernelT>
 int active_clusters(KernelT kernel, int csize, int smem, int threads)
 {
@@ -222,7 +222,10 @@ int active_clusters(KernelT kernel, int csize, int smem, int threads)
     };
     static Answers<Asked, 256> cache;
     int dev = 0, n = 0;
-    cudaGetDevice(&dev);
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
     const Asked asked{reinterpret_cast<const void *>(kernel), dev, csize, smem, threads};
     if (cache.find(asked, n))
         return n;
@@ -239,7 +242,7 @@ int active_clusters(KernelT kernel, int csize, int smem, int threads)
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();
-        n = 0;
+        return 0;  // of this call alone: the next one asks again
     }
     cache.keep(asked, n);
     return n;
