@@ -4,7 +4,9 @@ on a machine without a GPU.  No kernel runs and no pointer is read.
 """
 import ctypes
 import os
+import shutil
 import subprocess
+import tempfile
 
 import w8a8_int8_gemm_channel_b200 as sq
 from w8a8_int8_gemm_channel_b200 import _build
@@ -18,6 +20,20 @@ def load(folder):
     path = os.path.join(str(folder), "libsq_fake.so")
     subprocess.check_call(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-Wl,-z,defs", "-I", include,
                            "-o", path, SOURCE, *_build.objects()])
+    return _open(path)
+
+
+def another(lib):
+    """The same library once more, as if nothing of it had been called."""
+    fd, path = tempfile.mkstemp(".so", dir=os.path.dirname(lib._name))
+    os.close(fd)
+    shutil.copy(lib._name, path)
+    new = _open(path)
+    os.remove(path)
+    return new
+
+
+def _open(path):
     lib = ctypes.CDLL(path)
     sq._declare(lib)
     lib.fake_launch_name.restype = ctypes.c_char_p

@@ -21,7 +21,7 @@ struct Launch {
 
 std::vector<std::pair<const void *, std::string>> functions, variables;
 std::vector<Launch> launches;
-int fail_at = -1, fail_queries = 0;
+int fail_at = -1, fail_queries = 0, fail_call = 0;
 bool no_memory = false;
 cudaError_t last = cudaSuccess;
 void *handle = nullptr;
@@ -33,6 +33,8 @@ struct Allow {  // the fake's own allocations
     Allow() { no_memory = false; }
     ~Allow() { no_memory = was; }
 };
+
+bool fails() { return fail_call > 0 && --fail_call == 0; }
 
 std::string name_of(const void *f)
 {
@@ -61,11 +63,13 @@ void fake_reset(int fail)  // the launch number `fail` fails (-1: none)
 {
     launches.clear();
     fail_at = fail;
-    fail_queries = 0;
+    fail_queries = fail_call = 0;
     no_memory = false;
     last = cudaSuccess;
 }
 void fake_fail_queries(int n) { fail_queries = n; }  // the next n occupancy queries fail
+void fake_fail_call(int n) { fail_call = n; }         // the n-th call of the runtime from here on fails, launches not counted
+int fake_calls_left() { return fail_call; }           // 0: it has failed
 void fake_no_memory(int on) { no_memory = on != 0; }  // operator new throws in the library's code
 int fake_launches() { return static_cast<int>(launches.size()); }
 const char *fake_launch_name(int i) { return launches[i].name.c_str(); }
@@ -97,17 +101,26 @@ unsigned __cudaPopCallConfiguration(dim3 *, dim3 *, size_t *, void *) { return c
 
 cudaError_t cudaGetDevice(int *d)
 {
+    if (fails())
+        return last = cudaErrorInvalidValue;
     *d = 0;
     return cudaSuccess;
 }
 cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr a, int)
 {
+    if (fails())
+        return last = cudaErrorInvalidValue;
     *v = a == cudaDevAttrMultiProcessorCount ? 148 : 0;
     return cudaSuccess;
 }
-cudaError_t cudaFuncSetAttribute(const void *, cudaFuncAttribute, int) { return cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(const void *, cudaFuncAttribute, int)
+{
+    return fails() ? last = cudaErrorInvalidValue : cudaSuccess;
+}
 cudaError_t cudaGetDriverEntryPoint(const char *, void **f, unsigned long long, cudaDriverEntryPointQueryResult *r)
 {
+    if (fails())
+        return last = cudaErrorInvalidValue;
     *f = reinterpret_cast<void *>(&encode_tiled);
     *r = cudaDriverEntryPointSuccess;
     return cudaSuccess;
@@ -121,6 +134,8 @@ cudaError_t cudaGetLastError()
 cudaError_t cudaPeekAtLastError() { return last; }
 cudaError_t cudaGetSymbolAddress(void **p, const void *symbol)
 {
+    if (fails())
+        return last = cudaErrorInvalidValue;
     *p = const_cast<void *>(symbol);
     return cudaSuccess;
 }
@@ -150,6 +165,8 @@ cudaError_t cudaMemcpyToSymbol(const void *symbol, const void *src, size_t n, si
 }
 cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int *n, const void *, int, size_t, unsigned)
 {
+    if (fails())
+        return last = cudaErrorInvalidValue;
     if (fail_queries > 0 && fail_queries-- > 0)
         return last = cudaErrorInvalidValue;
     *n = 1;
@@ -157,6 +174,8 @@ cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int *n, const
 }
 cudaError_t cudaOccupancyMaxActiveClusters(int *n, const void *, const cudaLaunchConfig_t *)
 {
+    if (fails())
+        return last = cudaErrorInvalidValue;
     if (fail_queries > 0 && fail_queries-- > 0)
         return last = cudaErrorInvalidValue;
     *n = 148 / 2;

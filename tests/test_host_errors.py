@@ -133,3 +133,34 @@ def test_a_failed_query_is_asked_again(lib):
         lib.fake_fail_queries(1)
         assert call() == sq.SQ_ERR_CUDA and lib.fake_launches() == 0
         assert call() == sq.SQ_OK and lib.fake_launches() > 0
+
+
+A = 0x7F0000001000
+FIRST_CALLS = {
+    "mx4_gemm_many": lambda lib: lib.sq_mx4_gemm(A, A, A, A, 300, 256, 256, A, 1, WS, 1 << 40, None),
+    "mx4_gemm_few": lambda lib: lib.sq_mx4_gemm(A, A, A, A, 8, 256, 256, A, 1, WS, 1 << 40, None),
+    "mx4_linear": lambda lib: lib.sq_mx4_linear(A, 1, A, A, A, 300, 256, 256, A, 1, WS, 1 << 40, None),
+    "mx4_moe": lambda lib: moe(lib)[0],
+    "mx4_quant": lambda lib: lib.sq_mx4_quant_weight(A, 0, 8, 256, None, A, A, None),
+    "residual_norm": lambda lib: lib.sq_residual_norm_quant_mx4(A, 1, 4000, 256, A, None, 1, 1.0, A, WS, A, 1e-5, A, A, None),
+    "quant_act": lambda lib: lib.sq_quant_act(A, 1, 2000, 1040, A, A, A, None),
+    "w8a8_gemm": lambda lib: lib.sq_w8a8_gemm(A, A, A, A, 2048, 4096, 4096, A, 1, None),
+    "linear_noalloc": lambda lib: lib.sq_linear_noalloc(A, 1, A, A, A, 8, 256, 256, A, 1, None),
+}
+
+
+@pytest.mark.parametrize("name", FIRST_CALLS)
+def test_an_error_of_the_runtime_is_one_calls_error(lib, name):
+    """Whichever call of the runtime fails in a first use, the next use works and is not told of it."""
+    call, n = FIRST_CALLS[name], 0
+    while True:
+        fresh = fake_cuda.another(lib)
+        n += 1
+        fresh.fake_reset(-1)
+        fresh.fake_fail_call(n)
+        st = call(fresh)
+        if fresh.fake_calls_left() > 0:  # fewer than n calls
+            break
+        assert st in (sq.SQ_OK, sq.SQ_ERR_CUDA), n
+        assert call(fresh) == sq.SQ_OK, f"after call {n} failed"
+    assert st == sq.SQ_OK and n > 1

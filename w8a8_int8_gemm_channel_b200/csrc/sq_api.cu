@@ -1024,7 +1024,7 @@ void *noalloc_scratch()
     static void *addr[kMaxDevices] = {};
     static std::mutex mu;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices)
         return nullptr;
     std::lock_guard<std::mutex> lk(mu);
     if (addr[dev] == nullptr) {

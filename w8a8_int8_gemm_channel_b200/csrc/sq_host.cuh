@@ -38,14 +38,14 @@ inline bool valid_dtype(sq_dtype dt) { return dt == SQ_F32 || dt == SQ_BF16; }
 
 inline size_t dtype_size(sq_dtype dt) { return dt == SQ_F32 ? 4 : 2; }
 
-inline sq_status launch_status()
+// Whether a call of the runtime succeeded; its error is taken from the runtime,
+// so that no later call is told of it.
+inline bool cuda_ok(cudaError_t e)
 {
-    cudaError_t e = cudaPeekAtLastError();
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return SQ_ERR_CUDA;
-    }
-    return SQ_OK;
+    if (e == cudaSuccess)
+        return true;
+    cudaGetLastError();
+    return false;
 }
 
 struct DeviceInfo {
@@ -58,12 +58,12 @@ bool device_info(DeviceInfo &info)
     static DeviceInfo cache[kMaxDevices];
     static std::mutex mu;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices)
         return false;
     std::lock_guard<std::mutex> lk(mu);
     if (!cache[dev].ok) {
         int sms = 0;
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        if (!cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
             return false;
         cache[dev].sms = sms;
         cache[dev].ok = true;
@@ -117,27 +117,24 @@ sq_status launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, int sme
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
-        cudaGetLastError();
-        return SQ_ERR_CUDA;
-    }
-    return launch_status();
+    return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...)) ? SQ_OK : SQ_ERR_CUDA;
 }
 
 // ---- tensor maps -----------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+    auto f = fn.load(std::memory_order_acquire);
+    if (f == nullptr) {  // the first call, and every one after a failure
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
+        if (cuda_ok(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q)) &&
+            q == cudaDriverEntryPointSuccess) {
+            f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+            fn.store(f, std::memory_order_release);
+        }
+    }
+    return f;
 }
 
 // int8 matrix [rows, cols] (cols contiguous, row pitch = cols bytes); box of
@@ -164,13 +161,12 @@ template <typename KernelT>
 bool ensure_smem_attr(KernelT kernel, int bytes, std::atomic<uint64_t> &done_mask)
 {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices)
         return false;
     const uint64_t bit = 1ull << dev;
     if (done_mask.load(std::memory_order_acquire) & bit)
         return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        cudaSuccess)
+    if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)))
         return false;
     done_mask.fetch_or(bit, std::memory_order_release);
     return true;
@@ -222,10 +218,8 @@ int active_clusters(KernelT kernel, int csize, int smem, int threads)
     };
     static Answers<Asked, 256> cache;
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
+    if (!cuda_ok(cudaGetDevice(&dev)))
         return 0;
-    }
     const Asked asked{reinterpret_cast<const void *>(kernel), dev, csize, smem, threads};
     if (cache.find(asked, n))
         return n;
@@ -240,10 +234,8 @@ int active_clusters(KernelT kernel, int csize, int smem, int threads)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
+    if (!cuda_ok(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)))
         return 0;  // of this call alone: the next one asks again
-    }
     cache.keep(asked, n);
     return n;
 }
