@@ -487,7 +487,9 @@ SQ_API sq_status sq_mx4_moe(const uint8_t *xq, const uint8_t *sx, const int32_t 
  *   gate [ceil(M / gate_tokens), K] dt or NULL, row m / gate_tokens for token m
  *   (gate_tokens >= M: one gate for all); c finite; g [K] fp32 (sq_fold_gamma
  *   folds the next linear's factors in); eps >= 0 finite.
- * K a multiple of 16 (32 for MXFP4), at most 32768 (bf16) or 16384 (fp32).
+ * K a multiple of 16 (32 for MXFP4), at most 32768 (bf16) or 16384 (fp32); M at
+ * most 2^24.  (int8: a maximum so small that its scale rounds to 0 gives zero
+ * codes.)
  */
 SQ_API sq_status sq_residual_norm_quant(const void *b, sq_dtype dt, int64_t M, int64_t K, const float *gamma,
                                         const void *gate, int64_t gate_tokens, float c, const void *r, void *r_out,

@@ -498,7 +498,7 @@ def sq_mx4_linear_workspace_size(M: int, N: int, K: int) -> int:
 
 
 def sq_mx4_linear(x, s, wq, sw, y, workspace=None, stream=None):
-    """y [M, N] = mx4(x / s) w^T (a workspace is allocated when none is given)."""
+    """y [M, N] = mx4(x * (1 / s)) w^T (a workspace is allocated when none is given)."""
     M, K = x.shape
     N = wq.shape[0]
     if y.shape != (M, N):
@@ -620,7 +620,7 @@ def linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
 
 
 def mx4_quantize(x, s=None, stream=None):
-    """Codes and scale tiles of the activations x [M, K], divided by s when given: returns (xq, sx)."""
+    """Codes and scale tiles of the activations x [M, K], times the rounded 1 / s when given: returns (xq, sx)."""
     torch = _torch()
     M, K = x.shape
     with _on(stream, x.device):
@@ -644,7 +644,7 @@ def mx4_prepare_weight(w, s=None, stream=None):
 
 
 def mx4_linear(x, s, wq, sw, out_dtype=None, workspace=None, stream=None):
-    """y = mx4(x / s) w^T with a torch-allocated output."""
+    """y = mx4(x * (1 / s)) w^T with a torch-allocated output."""
     with _on(stream, x.device):
         y = _torch().empty(x.shape[0], wq.shape[0], dtype=out_dtype or x.dtype, device=x.device)
     sq_mx4_linear(x, s, wq, sw, y, workspace, stream)

@@ -256,6 +256,9 @@ int active_clusters(KernelT kernel, int csize, int smem, int threads)
 // a CTA at no modelled reduction cost; costed like the rest they take fewer,
 // longer ranges (64 x 1024 x 2048: 44 -> 19 us; 1 x 1040 x 3088: 21.5 ->
 // 17.4 us; 128 x 2048 x 8192: 54 -> 40 us).
+// The MXFP4 product takes the same rule with its own units (256 values of K, 16 KB
+// too).  Its costs were not fitted; the choice was measured at one shape only
+// (sq_mx4_stream.cuh).
 constexpr int64_t kDecodeEpiUnits = 4;
 inline int64_t decode_epi_units(int64_t M, int64_t S) { return kDecodeEpiUnits + (1 + std::min<int64_t>(M, 64) / 8) * S; }
 

@@ -30,7 +30,7 @@
 // 1408: 80 -> 78 us the layer).
 //
 // Measured (B200, calls one after another, this kernel and the second half): one
-// token, 2 experts of 4096 x 14336, 46 us; 16 tokens, 80 experts of 2048 x 768, 53
+// token, 2 experts of 4096 x 14336, 46 us; 16 tokens, 80 experts of 2048 x 768, 54
 // us; 64 tokens, 64 experts of 2048 x 1408, 72 us; the weights alone take 29, 32 and
 // 45 us at the copy rate.  This kernel streams at 5 to 6 TB/s once it runs; what
 // is left is fixed: finding the experts (1.3 us), the first loads (2 to 6 us),
@@ -112,7 +112,8 @@ __device__ __forceinline__ uint32_t mx4_code1(float v)
 // d needs no guards, so one Newton step on the quotient from the approximate
 // reciprocal stands in for the IEEE division, a long sequence (46 tokens, 40
 // experts of 384 x 6112: 93 -> 86 us).  In units of 2^-24: 2 from e^x, 1 each from
-// n and d, a little over 1 from the step.  An infinite v gives a NaN and so a NaN
+// n and d, a little over 1 from the step; below v = -87 e^x is subnormal and has
+// fewer bits (|v e^v| < 2^-118 there).  An infinite v gives a NaN and so a NaN
 // block, as the formula's infinity or NaN does.
 __device__ __forceinline__ float mx4_silu(float v)
 {

@@ -31,12 +31,16 @@
 // accumulates while the epilogue drains one.
 //
 // Measured (B200, with the quantiser before it, calls in a graph): 1 x 6144 x 4096
-// 11.8 us, 32 x 28672 x 4096 18.1 us (3.4 TB/s of weights; the weights' floor is
-// 10 us), 128 x 28672 x 4096 22.3 us.  A unit takes 320 ns once the stream runs;
+// 10.9 us, 32 x 28672 x 4096 16.3 us (3.8 TB/s of weights; the weights' floor is
+// 10 us), 128 x 28672 x 4096 20.3 us.  A unit takes 320 ns once the stream runs;
 // the rest is the quantiser and its boundary (5 us), the first loads (2.7 us) and
 // a shared tile's sum (3 us).  As many CTAs as SMs with tiles shared unevenly
-// (21 us), and weight loads before the wait for the quantiser (20.8 us) are
-// slower than the plan stream_ctas picks.
+// (21 us), and weight loads before the wait for the quantiser (20.8 us) were
+// slower at 32 x 28672 x 4096, when it took 20, than the plan stream_ctas picks.
+// The experts' second half streams slower, 2.5 TB/s (27.6 us for 69 MB, 16 tokens,
+// 8 of 128 experts of 2048 x 768, cold): for every tile and expert its four epilogue
+// warps read the choices again, wait for one another and drain 32 columns of four
+// accumulators for the one or two tokens that chose it.
 #pragma once
 
 #include <cstdint>

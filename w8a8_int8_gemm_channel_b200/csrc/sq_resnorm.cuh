@@ -16,10 +16,17 @@
 // factors gamma and g, 8 bytes a value against the 6.6 a bf16 value moves, would
 // make L2 the bound if every row fetched them; with several rows a CTA they are
 // staged in shared memory once, and the next row's loads are in flight while the
-// present row is reduced.  Bound: issue slots (33 instructions a value, the fp64
-// squares and the reductions' shuffles among them) and the latency of the
-// reductions: 4096 x 8192 bf16 in 64 us, 3.4 TB/s; two CTAs of 256 threads with
-// the next row in flight, against 71 us for three without and 68 for two of 512.
+// present row is reduced.
+//
+// Bound: latency.  At 4096 x 8192 bf16 (MXFP4, 64 us, 3.4 TB/s) 53 % of the issue
+// slots are taken (33 instructions a value) and no pipe is busy (ALU 33 %, XU 29 %,
+// fp64 10 %), with 16 warps an SM, as many as registers and shared memory allow.
+// The warps wait for short-scoreboard results and fixed latencies: unpacking, fp64
+// squares and two reductions are a serial chain a row, and half of the factors'
+// shared-memory wavefronts are bank conflicts (a lane's two float4 lie 32 bytes
+// from the next lane's).  Two CTAs of 256 threads with the next row in flight,
+// against 71 us for three without and 68 for two of 512.  The int8 form takes 87 us:
+// it forms a row's values twice, for the maximum and for the codes.
 #pragma once
 
 #include <cstdint>
