@@ -8,6 +8,7 @@ and where each entry point is launched; on the GPU the given stream is held back
 while the current one allocates and writes.
 """
 import contextlib
+import threading
 import types
 
 import numpy as np
@@ -180,3 +181,73 @@ def test_the_current_stream_allocates_and_writes_meanwhile(gpu, as_handle):
             assert torch.equal(y, w)
         for b in late:
             assert (b == 0x3C).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [False, True])
+def test_calls_that_allocate_are_captured(gpu, given):
+    """Workspaces and outputs made during a capture belong to the graph; replays give the eager bits."""
+    T, H, I, E = 17, 288, 160, 4
+    g = torch.Generator().manual_seed(2)
+    r = lambda *shape: (torch.randn(*shape, generator=g) * 0.1).cuda()  # noqa: E731
+    weights = [x for shape in ((E, I, H), (E, I, H), (E, H, I)) for x in sq.mx4_prepare_weight(r(*shape))]
+    wq, sw = sq.mx4_prepare_weight(r(1040, H))
+    ids = (torch.arange(2 * T, device="cuda").reshape(T, 2) % E).to(torch.int32)
+    share, x = torch.rand(T, 2, generator=g).cuda(), r(T, H)
+
+    def calls(**k):
+        xq, sx = sq.mx4_quantize(x, **k)
+        return sq.mx4_linear(x, None, wq, sw, **k), sq.mx4_moe(xq, sx, ids, share, *weights, out_dtype=F32, **k)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ys = calls(stream=side) if given else calls()
+    for seed in range(3):
+        x.copy_(torch.randn(T, H, generator=torch.Generator().manual_seed(seed)))
+        for y in ys:
+            y.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for y, want in zip(ys, calls()):
+            assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
+def test_host_threads_side_by_side(gpu):
+    """Threads on streams of their own, each with first calls of other shapes, and without workspaces of theirs."""
+    shapes = [(3, 544, 160), (40, 288, 416), (100, 256, 96), (1, 1056, 288)]
+
+    def work(T, H, I, seed):
+        g = torch.Generator().manual_seed(seed)
+        r = lambda *shape: (torch.randn(*shape, generator=g) * 0.1).cuda()  # noqa: E731
+        weights = [x for shape in ((5, I, H), (5, I, H), (5, H, I)) for x in sq.mx4_prepare_weight(r(*shape))]
+        wq, sw = sq.mx4_prepare_weight(r(528, H))
+        x, ids, share = r(T, H), (torch.arange(2 * T).reshape(T, 2) % 5).to(torch.int32).cuda(), torch.rand(T, 2, generator=g).cuda()
+        ys = []
+        for _ in range(30):
+            xq, sx = sq.mx4_quantize(x)
+            ys.append((sq.mx4_linear(x, None, wq, sw), sq.mx4_moe(xq, sx, ids, share, *weights, out_dtype=F32)))
+        torch.cuda.current_stream().synchronize()
+        return ys
+
+    out = [None] * len(shapes)
+
+    def thread(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out[i] = work(*shapes[i], i)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(len(shapes))]
+    for t_ in threads:
+        t_.start()
+    for t_ in threads:
+        t_.join()
+    for i, shape in enumerate(shapes):
+        want = work(*shape, i)[0]
+        assert out[i] is not None
+        for ys in out[i]:
+            assert all(torch.equal(y, w) for y, w in zip(ys, want))

@@ -212,9 +212,10 @@ __device__ __forceinline__ void mx4_zero_pad(uint8_t *scales, int rows, int KT, 
 // / TX rows at a time.  Memory-bound for fp32 (4096 x 8192 at 5.3 TB/s); with
 // bf16's 2.5 bytes a value the instructions count too (69 % of the issue slots and
 // 66 % of the ALU pipe taken), so the maximum takes three operands an instruction
-// and the products are packed: 28672 x 4096 in 64 us, 4.6 TB/s.  (16 columns a thread halve the shuffles but spread each load over twice
-// the lines: 94 us.)  The smoothing divides by multiplying with RN(1 / s), one division a
-// column and band instead of one a value.
+// and the products are packed: 28672 x 4096 in 64 us, 4.6 TB/s.  (16 columns a
+// thread halve the shuffles but spread each load over twice the lines: 94 us.)  The
+// smoothing divides by multiplying with RN(1 / s), one division a column and band
+// instead of one a value.
 // `zero`: tile counts of the product after it, cleared on the side.
 template <typename T, int OP>
 __global__ void __launch_bounds__(kMx4Threads) mx4_quant_kernel(const T *__restrict__ x, int rows, int K,
